@@ -451,6 +451,118 @@ gr_status gr_beam_backward_scatter(gr_beam* beam, int32_t step, const int32_t* d
                                    const int32_t* d_path_token, const float* d_weight, float* d_grad,
                                    int64_t grad_row_stride, gr_stream stream);
 
+/* ------------------------------------------------ the vocabulary's two ends */
+
+/*
+ * What a model does with the vocabulary on either side of a beam step: the
+ * step's tokens are looked up in the embedding table, and rows of hidden
+ * states are scored against the head's table.  Both tables are [vocab, dim]
+ * (one tensor when they are tied), and both gradients below can be added to
+ * one gradient.
+ *
+ * Common to gr_embed and gr_head:
+ *   - Tables, rows and their gradients are device arrays of one element type
+ *     (the handle's dtype), with rows of `dim` consecutive elements and a
+ *     row stride in elements (0 = dim; else dim <= stride <= 2^22).  No
+ *     alignment beyond the element's is needed; 16-byte aligned rows are
+ *     faster.  Outputs must not overlap inputs or each other.
+ *   - A token or target outside [0, vocab) (the -1 of finished and empty
+ *     slots, padding) stands for nothing: its row of a lookup is zero, its
+ *     loss is zero, it adds nothing to a gradient, and what its row of
+ *     hidden states or gradients holds (NaN too) is not used.
+ *   - Sums are held in 32 bits and each result is rounded once; results do
+ *     not depend on scheduling (no floating-point atomics).
+ *   - The handle owns its workspace, allocated on the device current at init
+ *     by the init call and nowhere else.  The other calls run on that device
+ *     whatever the current one is, allocate nothing, never synchronise, and
+ *     may be captured into a graph.  A handle must not be used from two
+ *     threads at once, nor by work that may overlap on the device: two
+ *     streams, or two captured graphs replayed at the same time.
+ *   - Errors: GR_ERR_INVALID_ARG for NULL pointers (unless stated), sizes,
+ *     strides or counts out of range; GR_ERR_OUT_OF_MEMORY from init;
+ *     GR_ERR_HIP if a launch fails.
+ */
+typedef struct gr_embed gr_embed;      /* opaque */
+typedef struct gr_head gr_head;        /* opaque */
+
+typedef struct {
+    int32_t vocab;       /* rows of the table, 1 <= vocab <= 2^30 */
+    int32_t dim;         /* elements of a row, 1 <= dim <= 65536 */
+    int32_t max_tokens;  /* most tokens of one call, 1 .. 2^24 */
+    int32_t dtype;       /* gr_dtype */
+    float scale;         /* finite, not zero */
+} gr_embed_config;
+
+gr_status gr_embed_init(const gr_embed_config* cfg, gr_stream stream, gr_embed** out);
+
+/*
+ * Rows of the table, scaled: out[i] = scale * weight[tokens[i]], computed in
+ * fp32 and rounded once.  d_tokens: int32 [n] (0 <= n <= max_tokens), e.g. a
+ * gr_beam's tokens of the last step.
+ */
+gr_status gr_embed_lookup(gr_embed* embed, const int32_t* d_tokens, int32_t n, const void* d_weight,
+                          int64_t weight_row_stride, void* d_out, int64_t out_row_stride, gr_stream stream);
+
+/*
+ * The table's gradient from the rows' gradient:
+ *   grad_weight[v] = scale * sum over i with tokens[i] = v of grad[i],
+ * every row of [vocab, dim] written (zero where no token is v).  With
+ * accumulate != 0 it is added to what d_grad_weight holds (one rounding of
+ * the sum), and rows without a token are left as they were.  Each word's
+ * rows are summed in fp32 in an order that depends on the tokens alone
+ * (ascending i within pieces, pieces in order).
+ */
+gr_status gr_embed_backward(gr_embed* embed, const int32_t* d_tokens, int32_t n, const void* d_grad,
+                            int64_t grad_row_stride, void* d_grad_weight, int64_t grad_weight_row_stride,
+                            int32_t accumulate, gr_stream stream);
+
+void gr_embed_free(gr_embed* embed);   /* NULL-safe; synchronises the device */
+
+typedef struct {
+    int32_t vocab;     /* words, 1 <= vocab <= 2^30 */
+    int32_t dim;       /* width of a hidden state, 1 <= dim <= 65536 */
+    int32_t max_rows;  /* most rows of one call, 1 .. 2^20 */
+    int32_t dtype;     /* gr_dtype */
+    float scale;       /* of the logits; finite, not zero */
+    int32_t score_only; /* != 0: no workspace for gr_head_backward, which is then refused */
+} gr_head_config;
+
+gr_status gr_head_init(const gr_head_config* cfg, gr_stream stream, gr_head** out);
+
+/*
+ * Softmax cross entropy of rows of hidden states against the head's table,
+ * without keeping the logits: with z[n][v] = scale * <hidden[n], weight[v]>
+ * (products of the elements summed in fp32),
+ *   lse[n]  = log sum_v exp(z[n][v])       (the normaliser of a beam step)
+ *   loss[n] = lse[n] - z[n][targets[n]]    (-log p of the target)
+ * and 0 for both where the target is outside [0, vocab).  d_targets: int32
+ * [n], d_loss, d_lse: fp32 [n], 0 <= n <= max_rows.  Any n from one row
+ * (scoring one hypothesis's next word) on.
+ */
+gr_status gr_head_loss(gr_head* head, const void* d_hidden, int64_t hidden_row_stride, const void* d_weight,
+                       int64_t weight_row_stride, const int32_t* d_targets, int32_t n, float* d_loss,
+                       float* d_lse, gr_stream stream);
+
+/*
+ * The loss's gradient.  With g[n] = d_grad_loss[n] (fp32, the upstream
+ * gradient of loss[n]; -weight / path weight for a search's path gradient),
+ *   G[n][v] = scale * g[n] * (exp(z[n][v] - lse[n]) - [v = targets[n]])
+ *   grad_hidden[n] = sum_v G[n][v] * weight[v]     (0 for rows without a target)
+ *   grad_weight[v] = sum_n G[n][v] * hidden[n]     (+ what it holds, if accumulate != 0)
+ * d_lse is gr_head_loss's of the same inputs.  The logits are computed again,
+ * a piece of the vocabulary at a time.  For bf16, a piece's G is rounded to
+ * bf16 before both products.  d_grad_hidden or d_grad_weight may be NULL
+ * (not both): that gradient is then not computed.  n = 0 writes zeros to
+ * grad_weight unless accumulate.  GR_ERR_UNSUPPORTED for a score_only head.
+ */
+gr_status gr_head_backward(gr_head* head, const void* d_hidden, int64_t hidden_row_stride, const void* d_weight,
+                           int64_t weight_row_stride, const int32_t* d_targets, int32_t n, const float* d_lse,
+                           const float* d_grad_loss, void* d_grad_hidden, int64_t grad_hidden_row_stride,
+                           void* d_grad_weight, int64_t grad_weight_row_stride, int32_t accumulate,
+                           gr_stream stream);
+
+void gr_head_free(gr_head* head);      /* NULL-safe; synchronises the device */
+
 /* ---------------------------------------------------------- observability */
 
 /*

@@ -20,9 +20,9 @@ from typing import Optional, Sequence
 import numpy as np
 
 from . import _lib
-from ._lib import BeamConfig, BeamView, StepIO, StepStats
+from ._lib import BeamConfig, BeamView, EmbedConfig, HeadConfig, StepIO, StepStats
 
-__all__ = ["GrError", "Trie", "Beam", "beam_step_static", "trie_validate", "probe_read", "probe_copy",
+__all__ = ["GrError", "Trie", "Beam", "Embedding", "Head", "beam_step_static", "trie_validate", "probe_read", "probe_copy",
            "probe_draw_error", "draw_error_bound", "version", "lib"]
 
 
@@ -331,6 +331,216 @@ class Beam:
             self.close()
         except Exception:
             pass
+
+
+class _Table:
+    """What Embedding and Head share: the table's sizes and element type, and
+    the checks of tensors against them."""
+
+    def _setup(self, vocab, dim, dtype, scale):
+        import torch
+        if dtype not in ("f32", "bf16"):
+            raise ValueError("dtype must be 'f32' or 'bf16'")
+        self.vocab, self.dim, self.dtype, self.scale = int(vocab), int(dim), dtype, float(scale)
+        self._torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self._gr_dtype = _lib.GR_BF16 if dtype == "bf16" else _lib.GR_F32
+        self._h = None
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise ValueError(f"{type(self).__name__.lower()} is closed")
+        return self._h
+
+    def _tensor(self, t, name, dtype):
+        import torch
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+            raise TypeError(f"{name} must be a cuda {dtype} tensor")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the {type(self).__name__.lower()} on {self.device}")
+        return t
+
+    def _flat(self, t, name, dtype, n=None):
+        """A contiguous tensor (of n elements): its address."""
+        t = self._tensor(t, name, dtype)
+        if not t.is_contiguous() or (n is not None and t.numel() != n):
+            raise ValueError(f"{name} must be contiguous" + (f" with {n} elements" if n is not None else ""))
+        return t.data_ptr()
+
+    def _rows(self, t, name, n):
+        """n rows of `dim` elements, [n, dim] with any row stride or contiguous
+        [..., dim]: their address and row stride."""
+        t = self._tensor(t, name, self._torch_dtype)
+        if t.dim() < 2 or t.shape[-1] != self.dim or t.numel() != n * self.dim:
+            raise ValueError(f"{name} must hold {n} rows of {self.dim}, not {tuple(t.shape)}")
+        if t.is_contiguous():
+            return t.data_ptr(), self.dim
+        if t.dim() != 2 or (self.dim > 1 and t.stride(1) != 1) or t.stride(0) < self.dim:
+            raise ValueError(f"{name} must be contiguous, or [n, dim] with rows of consecutive elements that do not overlap")
+        return t.data_ptr(), t.stride(0)
+
+    def _stream(self, stream):
+        """The torch stream to enqueue on (default: the current one of the
+        handle's device)."""
+        import torch
+        if stream is None:
+            return torch.cuda.current_stream(self.device)
+        if hasattr(stream, "cuda_stream"):
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the {type(self).__name__.lower()} on {self.device}")
+            return stream
+        return torch.cuda.ExternalStream(int(stream), device=self.device)
+
+    def _empty(self, shape, dtype, s):
+        """A new output, owned by the stream that writes it."""
+        import torch
+        with torch.cuda.stream(s):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _used(self, s, *tensors):
+        """Tensors of the caller's current stream that work on `s` reads or
+        writes: their memory is not reused before that work is done."""
+        import torch
+        if s != torch.cuda.current_stream(self.device):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+
+    def close(self):
+        if getattr(self, "_h", None) is not None:
+            self._free(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Embedding(_Table):
+    """Rows of a [vocab, dim] table for token ids, times `scale`, and the
+    table's gradient (gr_embed_*).  Tokens outside [0, vocab), such as the -1 of
+    finished and empty beam slots, get a row of zeros and no gradient.
+    max_tokens: the most tokens of one call."""
+
+    def __init__(self, vocab: int, dim: int, max_tokens: int, *, dtype: str = "f32", scale: float = 1.0, stream=None):
+        import torch
+        self._setup(vocab, dim, dtype, scale)
+        self.max_tokens = int(max_tokens)
+        self._free = lib().gr_embed_free
+        cfg = EmbedConfig(vocab=self.vocab, dim=self.dim, max_tokens=self.max_tokens, dtype=self._gr_dtype,
+                          scale=self.scale)
+        h = C.c_void_p()
+        _check(lib().gr_embed_init(C.byref(cfg), None if stream is None else _stream_ptr(stream), C.byref(h)))
+        self._h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def lookup(self, tokens, weight, out=None, stream=None):
+        """scale * weight[tokens]: tokens a contiguous cuda int32 tensor of any
+        shape, weight [vocab, dim]; returns [*tokens.shape, dim] (`out`, if given)."""
+        import torch
+        pt = self._flat(tokens, "tokens", torch.int32)
+        n = tokens.numel()
+        pw, sw = self._rows(weight, "weight", self.vocab)
+        s = self._stream(stream)
+        if out is None:
+            out = self._empty((*tokens.shape, self.dim), self._torch_dtype, s)
+        po, so = self._rows(out, "out", n)
+        _check(lib().gr_embed_lookup(self.handle, pt, n, pw, sw, po, so, s.cuda_stream))
+        self._used(s, tokens, weight)
+        return out
+
+    def backward(self, tokens, grad, grad_weight=None, accumulate: bool = False, stream=None):
+        """The table's gradient [vocab, dim] from grad [*tokens.shape, dim], the
+        gradient of lookup's result.  grad_weight: written whole, or added to
+        with accumulate=True; a new tensor if None."""
+        import torch
+        pt = self._flat(tokens, "tokens", torch.int32)
+        n = tokens.numel()
+        pg, sg = self._rows(grad, "grad", n)
+        s = self._stream(stream)
+        if grad_weight is None:
+            if accumulate:
+                raise ValueError("accumulate needs the grad_weight to add to")
+            grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, s)
+        pw, sw = self._rows(grad_weight, "grad_weight", self.vocab)
+        _check(lib().gr_embed_backward(self.handle, pt, n, pg, sg, pw, sw, 1 if accumulate else 0, s.cuda_stream))
+        self._used(s, tokens, grad, grad_weight)
+        return grad_weight
+
+
+class Head(_Table):
+    """Softmax cross entropy of hidden states against a [vocab, dim] table
+    without keeping the logits, and its gradient (gr_head_*).  Rows whose target
+    is outside [0, vocab) have loss 0 and no gradient.  max_rows: the most rows
+    of one call; backward=False: no workspace for the gradient."""
+
+    def __init__(self, vocab: int, dim: int, max_rows: int, *, dtype: str = "f32", scale: float = 1.0,
+                 backward: bool = True, stream=None):
+        import torch
+        self._setup(vocab, dim, dtype, scale)
+        self.max_rows = int(max_rows)
+        self._free = lib().gr_head_free
+        cfg = HeadConfig(vocab=self.vocab, dim=self.dim, max_rows=self.max_rows, dtype=self._gr_dtype,
+                         scale=self.scale, score_only=0 if backward else 1)
+        h = C.c_void_p()
+        _check(lib().gr_head_init(C.byref(cfg), None if stream is None else _stream_ptr(stream), C.byref(h)))
+        self._h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def loss(self, hidden, weight, targets, stream=None):
+        """(loss, lse), float32 of targets' shape: -log p of each row's target
+        and the row's log-softmax normaliser.  hidden [*targets.shape, dim],
+        weight [vocab, dim], targets a contiguous cuda int32 tensor."""
+        import torch
+        pt = self._flat(targets, "targets", torch.int32)
+        n = targets.numel()
+        ph, sh = self._rows(hidden, "hidden", n)
+        pw, sw = self._rows(weight, "weight", self.vocab)
+        s = self._stream(stream)
+        loss, lse = (self._empty(targets.shape, torch.float32, s) for _ in range(2))
+        _check(lib().gr_head_loss(self.handle, ph, sh, pw, sw, pt, n, loss.data_ptr(), lse.data_ptr(), s.cuda_stream))
+        self._used(s, hidden, weight, targets)
+        return loss, lse
+
+    def backward(self, hidden, weight, targets, lse, grad_loss, grad_hidden=None, grad_weight=None,
+                 accumulate: bool = False, stream=None, need: Sequence[str] = ("hidden", "weight")):
+        """(grad_hidden, grad_weight) of the loss, given the upstream gradient
+        grad_loss (float32, targets' shape) and loss()'s lse.  grad_hidden,
+        grad_weight: tensors to write (new ones if None); accumulate=True adds
+        to grad_weight.  need: which of the two to compute; the other is None."""
+        import torch
+        pt = self._flat(targets, "targets", torch.int32)
+        n = targets.numel()
+        ph, sh = self._rows(hidden, "hidden", n)
+        pw, sw = self._rows(weight, "weight", self.vocab)
+        pl = self._flat(lse, "lse", torch.float32, n)
+        pg = self._flat(grad_loss, "grad_loss", torch.float32, n)
+        need = set(need)
+        if not need or not need <= {"hidden", "weight"}:
+            raise ValueError("need names 'hidden', 'weight' or both")
+        s = self._stream(stream)
+        pgh = pgw = None
+        sgh = sgw = 0
+        if "hidden" not in need:
+            grad_hidden = None
+        else:
+            if grad_hidden is None:
+                grad_hidden = self._empty(hidden.shape, self._torch_dtype, s)
+            pgh, sgh = self._rows(grad_hidden, "grad_hidden", n)
+        if "weight" not in need:
+            grad_weight = None
+        else:
+            if grad_weight is None:
+                if accumulate:
+                    raise ValueError("accumulate needs the grad_weight to add to")
+                grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, s)
+            pgw, sgw = self._rows(grad_weight, "grad_weight", self.vocab)
+        _check(lib().gr_head_backward(self.handle, ph, sh, pw, sw, pt, n, pl, pg, pgh, sgh, pgw, sgw,
+                                      1 if accumulate else 0, s.cuda_stream))
+        self._used(s, hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
+        return grad_hidden, grad_weight
 
 
 def beam_step_static(batch: int, beam_width: int, vocab: int, max_steps: int, step: int, logits,

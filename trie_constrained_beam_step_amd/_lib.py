@@ -49,6 +49,16 @@ class StepStats(C.Structure):
                 ("fused_requests", C.c_int64)]
 
 
+class EmbedConfig(C.Structure):
+    _fields_ = [("vocab", C.c_int32), ("dim", C.c_int32), ("max_tokens", C.c_int32), ("dtype", C.c_int32),
+                ("scale", C.c_float)]
+
+
+class HeadConfig(C.Structure):
+    _fields_ = [("vocab", C.c_int32), ("dim", C.c_int32), ("max_rows", C.c_int32), ("dtype", C.c_int32),
+                ("scale", C.c_float), ("score_only", C.c_int32)]
+
+
 _VP = C.c_void_p
 _I32, _I64, _SZ = C.c_int32, C.c_int64, C.c_size_t
 _PP = C.POINTER(C.c_void_p)
@@ -68,6 +78,15 @@ SIGNATURES = {
     "gr_beam_step_static": (C.c_int, [C.POINTER(StepIO), _VP]),
     "gr_beam_backward": (C.c_int, [_VP, _VP, _VP, _VP, _VP, _VP]),
     "gr_beam_backward_scatter": (C.c_int, [_VP, C.c_int32, _VP, _VP, _VP, _VP, C.c_int64, _VP]),
+    "gr_embed_init": (C.c_int, [C.POINTER(EmbedConfig), _VP, C.POINTER(_VP)]),
+    "gr_embed_lookup": (C.c_int, [_VP, _VP, _I32, _VP, _I64, _VP, _I64, _VP]),
+    "gr_embed_backward": (C.c_int, [_VP, _VP, _I32, _VP, _I64, _VP, _I64, _I32, _VP]),
+    "gr_embed_free": (None, [_VP]),
+    "gr_head_init": (C.c_int, [C.POINTER(HeadConfig), _VP, C.POINTER(_VP)]),
+    "gr_head_loss": (C.c_int, [_VP, _VP, _I64, _VP, _I64, _VP, _I32, _VP, _VP, _VP]),
+    "gr_head_backward": (C.c_int, [_VP, _VP, _I64, _VP, _I64, _VP, _I32, _VP, _VP, _VP, _I64, _VP, _I64, _I32,
+                                   _VP]),
+    "gr_head_free": (None, [_VP]),
     "gr_beam_view_get": (C.c_int, [_VP, C.POINTER(BeamView)]),
     "gr_beam_set_state": (C.c_int, [_VP, _I32, _VP, _VP, _VP, _VP, _VP]),
     "gr_beam_free": (None, [_VP]),

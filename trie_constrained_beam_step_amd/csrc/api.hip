@@ -18,14 +18,19 @@
 #include <cmath>
 #include "internal.h"
 #include "backward.h"
+#include "errors.h"
 
+using gr::fail;
+using gr::hip_fail;
 using gr::StepArgs;
 
 namespace {
 
 thread_local std::string g_err;
 
-gr_status fail(gr_status s, const char* fmt, ...) {
+}  // namespace
+
+gr_status gr::fail(gr_status s, const char* fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -35,15 +40,11 @@ gr_status fail(gr_status s, const char* fmt, ...) {
     return s;
 }
 
-gr_status hip_fail(hipError_t e, const char* what) {
+gr_status gr::hip_fail(hipError_t e, const char* what) {
     return fail(GR_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-#define HIP_TRY(expr, what)                       \
-    do {                                          \
-        hipError_t e_ = (expr);                   \
-        if (e_ != hipSuccess) return hip_fail(e_, what); \
-    } while (0)
+namespace {
 
 template <typename T>
 hipError_t dalloc(T** p, size_t count) {
