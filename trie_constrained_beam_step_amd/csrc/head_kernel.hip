@@ -2,197 +2,595 @@
 // table, without keeping the logits, and its gradient.
 //
 // With z[n][v] = scale * <h_n, w_v>:
-//   forward   z in tiles; a tile leaves each of its rows' (max, sum of
-//             exp(z - max)); a second kernel joins a row's tiles.
+//   forward   z in tiles on the matrix cores; a wave of a tile leaves, for each
+//             of its rows, (max, sum of exp(z - max)) over its words: a part.
+//             A second kernel joins a row's parts.
 //   backward  a piece of the vocabulary at a time: z again, G = scale * g *
 //             (exp(z - lse) - onehot) into the workspace, then the piece's
 //             share of grad_hidden = G W and its rows of grad_weight = G^T H.
+// All three products are gemm_tile.h's, with the words (first product) or the
+// width (the others) as its rows m and the hidden states (or words) as its n.
+//
+// Rows without a target are left out at the start (pack_rows_kernel): the
+// products run over the packed rows only, whose number is known on the device
+// alone, so grids are sized for all rows and workgroups behind the count end
+// at once.
 #include "device_common.h"
+#include "gemm_tile.h"
 #include "gr.h"
 #include "vocab.h"
 
 namespace gr {
 namespace {
 
-constexpr int kT = kHeadTile;  // 64 x 64 tiles, 256 threads, 4 x 4 per thread
-constexpr int kK = 16;
-
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ void store_elem(float* p, int64_t i, float v) { p[i] = v; }
-// bf16 with round to nearest even; NaN stays NaN
-__device__ __forceinline__ void store_elem(uint16_t* p, int64_t i, float v) {
-    const uint32_t b = __float_as_uint(v);
-    p[i] = (v != v) ? (uint16_t)((b >> 16) | 0x40) : (uint16_t)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
+__device__ __forceinline__ void store_elem(uint16_t* p, int64_t i, float v) { p[i] = bf16_bits(v); }
+
+// x as PL bf16 planes (gemm_tile.h).  A value whose first plane would round to
+// infinity takes the largest finite one, and the others carry the rest.
+template <int PL>
+__device__ __forceinline__ void split_planes(float x, uint16_t (&out)[PL]) {
+    out[0] = bf16_bits(x);
+    if (PL == 1) return;
+    if ((out[0] & 0x7FFF) == 0x7F80 && fabsf(x) < INFINITY) out[0] = (uint16_t)((out[0] & 0x8000) | 0x7F7F);
+    float rest = fabsf(x) < INFINITY ? x - bf16_value(out[0]) : 0.0f;  // inf, NaN: the first plane alone
+#pragma unroll
+    for (int p = 1; p < PL; ++p) {
+        out[p] = bf16_bits(rest);
+        rest -= bf16_value(out[p]);
+    }
 }
 
 __device__ __forceinline__ bool has_target(const HeadArgs& a, int n) {
     return n < a.N && a.targets[n] >= 0 && a.targets[n] < a.V;
 }
 
-// c[i][j] = sum_k A(m0 + ty*4 + i, k) * B(n0 + tx*4 + j, k), k < K
-template <typename FA, typename FB>
-__device__ void tile_product(int K, FA fa, FB fb, float c[4][4]) {
-    __shared__ float sa[kK][kT + 1], sb[kK][kT + 1];
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
-    for (int k0 = 0; k0 < K; k0 += kK) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < kK * kT; e += 256) {
-            const int k = e % kK, r = e / kK;
-            sa[k][r] = k0 + k < K ? fa(r, k0 + k) : 0.0f;
-            sb[k][r] = k0 + k < K ? fb(r, k0 + k) : 0.0f;
-        }
-        __syncthreads();
-        for (int k = 0; k < kK; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) c[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], c[i][j]);
+// ------------------------------------------------------------ packing
+
+// Row `src` of D elements into PL planes of Dp.
+template <typename T, int PL>
+__device__ __forceinline__ void pack_row(const T* src, int D, int Dp, uint16_t* dst, int64_t plane, int lane, int lanes) {
+    for (int d = lane; d < Dp; d += lanes) {
+        uint16_t b[PL];
+        split_planes<PL>(d < D ? load_elem(src, d) : 0.0f, b);
+#pragma unroll
+        for (int p = 0; p < PL; ++p) dst[p * plane + d] = b[p];
     }
 }
 
-// logits of words v0 .. v0+63 (rows of c) and hidden states n0 .. n0+63
-template <typename T>
-__device__ void logits_tile(const HeadArgs& a, int v0, int n0, float c[4][4]) {
-    tile_product(
-        a.D,
-        [&](int r, int k) { return v0 + r < a.V ? load_elem((const T*)a.weight + (int64_t)(v0 + r) * a.wstride, k) : 0.0f; },
-        [&](int r, int k) {
-            return has_target(a, n0 + r) ? load_elem((const T*)a.hidden + (int64_t)(n0 + r) * a.hstride, k) : 0.0f;
-        },
-        c);
-}
+constexpr int kPackRows = 16;  // rows of a workgroup
 
-template <typename T>
-__global__ __launch_bounds__(256) void head_parts_kernel(HeadArgs a) {
-    __shared__ float z[kT][kT + 1];
-    const int v0 = blockIdx.x * kT, n0 = blockIdx.y * kT;
-    float c[4][4];
-    logits_tile<T>(a, v0, n0, c);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) z[tx * 4 + j][ty * 4 + i] = c[i][j] * a.scale;
+// The rows that have a target, packed in order.  Each workgroup counts the
+// targets before its own rows by itself (the targets of 2^16 rows are 256 KB
+// of L2 reads; a scan kernel before this one would cost a launch).
+template <typename T, int PL>
+__global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows_cap, int rows_per_wg) {
+    __shared__ int wsum[4], base;
+    const int r0 = blockIdx.x * rows_per_wg;
+    int c = 0;
+    for (int i = threadIdx.x; i < r0; i += 256) c += has_target(a, i) ? 1 : 0;
+    c = (int)wave_sum_ll(c);
+    if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = c;
     __syncthreads();
-    if (threadIdx.x < kT && has_target(a, n0 + threadIdx.x)) {
-        const int n = n0 + threadIdx.x, nv = min(kT, a.V - v0);
-        float m = kFarBelow, s = 0.0f;
-        for (int v = 0; v < nv; ++v) m = fmaxf(m, z[threadIdx.x][v]);
-        for (int v = 0; v < nv; ++v) s += expf(z[threadIdx.x][v] - m);
-        a.parts[(int64_t)blockIdx.x * a.N + n] = make_float2(m, s);
-        const int t = a.targets[n] - v0;
-        if (t >= 0 && t < nv) a.zt[n] = z[threadIdx.x][t];
+    if (threadIdx.x == 0) base = wsum[0] + wsum[1] + wsum[2] + wsum[3];
+    __syncthreads();
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int r2 = min(r0 + rows_per_wg, a.N);
+    int before = base;
+    for (int r1 = r0; r1 < r2; r1 += 64) {
+        const int mine = r1 + lane;
+        const bool ok = mine < r2 && has_target(a, mine);
+        const uint64_t m = __ballot(ok);
+        if (wave == 0 && mine < r2) {
+            const int at = ok ? before + lanes_below(m) : -1;
+            a.ws.place[mine] = at;
+            if (ok) {
+                a.ws.target[at] = a.targets[mine];
+                if (a.grad_loss) {
+                    a.ws.gscale[at] = a.scale * a.grad_loss[mine];
+                    a.ws.lse[at] = a.lse_in[mine];
+                }
+            }
+        }
+        int k = 0;
+        for (uint64_t rest = m; rest; rest &= rest - 1, ++k) {
+            if ((k & 3) != wave) continue;
+            const int row = r1 + __builtin_ctzll(rest);
+            pack_row<T, PL>((const T*)a.hidden + (int64_t)row * a.hstride, a.D, a.plan.Dp,
+                            a.ws.H + (int64_t)(before + k) * a.plan.Dp, rows_cap * a.plan.Dp, lane, 64);
+        }
+        before += __popcll(m);
+    }
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *a.ws.count = before;
+}
+
+// Words [v0, v0 + nv) of the table in planes.
+template <typename T, int PL>
+__global__ __launch_bounds__(256) void pack_words_kernel(HeadArgs a, int v0, int nv) {
+    const int v = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (v >= nv) return;
+    pack_row<T, PL>((const T*)a.weight + (int64_t)(v0 + v) * a.wstride, a.D, a.plan.Dp, a.ws.W + (int64_t)v * a.plan.Dp,
+                    (int64_t)a.plan.Vw * a.plan.Dp, threadIdx.x & 63, 64);
+}
+
+// ----------------------------------------------------------- tile order
+
+__host__ __device__ inline int tiles_of(int64_t x, int t) { return (int)((x + t - 1) / t); }
+
+// Workgroup b of tm x tn tiles: workgroups b, b + 8, ... run on one XCD (its own
+// L2), so each XCD takes a contiguous run of tiles, in groups of 8 tile rows
+// whose columns follow one another.
+__device__ __forceinline__ void tile_of(int b, int tm, int tn, int& im, int& in) {
+    const int total = tm * tn, q = total / 8, rem = total % 8, x = b % 8;
+    const int id = x * q + (x < rem ? x : rem) + b / 8;
+    const int per = 8 * tn, g = id / per, first = g * 8;
+    const int gm = tm - first < 8 ? tm - first : 8;
+    im = first + (id % per) % gm;
+    in = (id % per) / gm;
+}
+
+// Shapes of the tiles by element type: large ones reuse each operand most,
+// small ones fill the chip where there are few large ones.
+template <typename T, bool AAcross, bool BAcross, bool Large>
+struct TileFor;
+template <bool AAcross, bool BAcross>
+struct TileFor<uint16_t, AAcross, BAcross, true> {
+    typedef GemmTile<256, 256, 128, 64, 64, 1, AAcross, BAcross> type;
+};
+template <bool AAcross, bool BAcross>
+struct TileFor<uint16_t, AAcross, BAcross, false> {
+    typedef GemmTile<128, 128, 64, 64, 64, 1, AAcross, BAcross> type;
+};
+template <bool AAcross, bool BAcross>
+struct TileFor<float, AAcross, BAcross, true> {
+    typedef GemmTile<256, 128, 64, 64, 32, 3, AAcross, BAcross> type;
+};
+template <bool AAcross, bool BAcross>
+struct TileFor<float, AAcross, BAcross, false> {
+    typedef GemmTile<128, 128, 64, 64, 32, 3, AAcross, BAcross> type;
+};
+
+__device__ __forceinline__ Operand hidden_operand(const HeadArgs& a, int64_t rows_cap, int count) {
+    return Operand{a.ws.H, a.plan.Dp, rows_cap * a.plan.Dp, (int64_t)count * a.plan.Dp};
+}
+__device__ __forceinline__ Operand grad_operand(const HeadArgs& a, int64_t rows_cap, int count) {
+    return Operand{a.ws.G, a.plan.Vg, rows_cap * a.plan.Vg, (int64_t)count * a.plan.Vg};
+}
+
+// --------------------------------------------------- logits and their uses
+
+// A wave's accumulators (gemm_tile.h): fragments 2i and 2i+1 of a lane hold the
+// eight words rm + 32*i + (lane/16)*8 + 0..7 of hidden state rn + 16*j + lane%16.
+
+template <typename Tile>
+__global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
+    __shared__ __align__(1024) char s0[Tile::Stage];
+    __shared__ __align__(1024) char s1[Tile::Stage];
+    const int count = *a.ws.count;
+    int im, in;
+    tile_of(blockIdx.x, tiles_of(nv, Tile::BM), tiles_of(a.N, Tile::BN), im, in);
+    const int m0 = im * Tile::BM, n0 = in * Tile::BN;
+    if (n0 >= count) return;
+    f32x4v acc[Tile::FM][Tile::FN] = {};
+    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, s0, s1, acc);
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
+    if (rm >= nv) return;
+    const int vl = vp + rm + (lane >> 4) * 8;  // word of acc[0][j][0]
+    const int part = (vp + rm) / Tile::WM;
+#pragma unroll
+    for (int j = 0; j < Tile::FN; ++j) {
+        const int n = rn + j * 16 + (lane & 15);
+        const int t = n < count ? a.ws.target[n] - vl : -1;
+        float m = kFarBelow;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int o = (i >> 1) * 32 + (i & 1) * 4 + r;
+                const float z = acc[i][j][r] * a.scale;
+                acc[i][j][r] = z;
+                if (vl + o < a.V) m = fmaxf(m, z);
+                if (o == t) a.ws.zt[n] = z;
+            }
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int o = (i >> 1) * 32 + (i & 1) * 4 + r;
+                const float e = ex2((acc[i][j][r] - m) * kLog2e);
+                if (vl + o < a.V) s += e;
+            }
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (lane < 16 && n < count) a.ws.parts[(int64_t)part * rows_cap + n] = make_float2(m, s);
     }
 }
 
-__global__ __launch_bounds__(256) void head_join_kernel(HeadArgs a, int tiles) {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N) return;
-    float loss = 0.0f, lse = 0.0f;
-    if (has_target(a, n)) {
-        float m = kFarBelow, s = 0.0f;
-        for (int i = 0; i < tiles; ++i) m = fmaxf(m, a.parts[(int64_t)i * a.N + n].x);
-        for (int i = 0; i < tiles; ++i) {
-            const float2 p = a.parts[(int64_t)i * a.N + n];
-            s += p.y * expf(p.x - m);
+// Loss and lse of each row from its parts: workgroups of `rb` rows, 1024 / rb
+// threads to a row.
+__global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t rows_cap, int parts, int rb) {
+    __shared__ float sm[1024], ss[1024];
+    const int slices = 1024 / rb, row = threadIdx.x % rb, slice = threadIdx.x / rb;
+    const int n = blockIdx.x * rb + row;
+    const int at = n < a.N ? a.ws.place[n] : -1;
+    float m = kFarBelow, s = 0.0f;
+    if (at >= 0)
+        for (int p = slice; p < parts; p += slices) {
+            const float2 x = a.ws.parts[(int64_t)p * rows_cap + at];
+            const float hi = fmaxf(m, x.x);
+            s = s * ex2((m - hi) * kLog2e) + x.y * ex2((x.x - hi) * kLog2e);
+            m = hi;
         }
-        lse = m + logf(s);
-        loss = lse - a.zt[n];
+    sm[threadIdx.x] = m;
+    ss[threadIdx.x] = s;
+    for (int half = slices / 2; half; half >>= 1) {
+        __syncthreads();
+        if (slice < half) {
+            const int o = threadIdx.x + half * rb;
+            const float hi = fmaxf(sm[threadIdx.x], sm[o]);
+            ss[threadIdx.x] = ss[threadIdx.x] * ex2((sm[threadIdx.x] - hi) * kLog2e) + ss[o] * ex2((sm[o] - hi) * kLog2e);
+            sm[threadIdx.x] = hi;
+        }
     }
-    a.loss[n] = loss;
-    a.lse[n] = lse;
-}
-
-template <typename T>
-__global__ __launch_bounds__(256) void head_logit_grad_kernel(HeadArgs a, int vp) {
-    const int v0 = vp + blockIdx.x * kT, n0 = blockIdx.y * kT;
-    float c[4][4];
-    logits_tile<T>(a, v0, n0, c);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
-        if (n >= a.N) continue;
-        const bool ok = has_target(a, n);
-        const float g = ok ? a.scale * a.grad_loss[n] : 0.0f, lse = ok ? a.lse[n] : 0.0f;
-        for (int i = 0; i < 4; ++i) {
-            const int v = v0 + ty * 4 + i;
-            if (v >= a.V) continue;
-            float p = expf(c[i][j] * a.scale - lse);
-            if (ok && v == a.targets[n]) p -= 1.0f;
-            a.G[(int64_t)n * a.Vp + (v - vp)] = ok ? g * p : 0.0f;
+    if (slice == 0 && n < a.N) {
+        float lse = 0.0f, loss = 0.0f;
+        if (at >= 0) {
+            lse = sm[row] + logf(ss[row]);
+            loss = lse - a.ws.zt[at];
         }
+        a.loss[n] = loss;
+        a.lse[n] = lse;
     }
 }
 
-// grad_hidden[n][d] += sum over the piece's words of G[n][v] W[v][d]
-template <typename T>
-__global__ __launch_bounds__(256) void head_ghidden_kernel(HeadArgs a, int vp, int nv, bool first, bool last) {
-    const int d0 = blockIdx.x * kT, n0 = blockIdx.y * kT;
-    float c[4][4];
-    tile_product(
-        nv, [&](int r, int k) { return d0 + r < a.D ? load_elem((const T*)a.weight + (int64_t)(vp + k) * a.wstride, d0 + r) : 0.0f; },
-        [&](int r, int k) { return n0 + r < a.N ? a.G[(int64_t)(n0 + r) * a.Vp + k] : 0.0f; }, c);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int j = 0; j < 4; ++j)
-        for (int i = 0; i < 4; ++i) {
-            const int n = n0 + tx * 4 + j, d = d0 + ty * 4 + i;
-            if (n >= a.N || d >= a.D) continue;
-            float* acc = a.gh_acc + (int64_t)n * a.D + d;
-            const float s = first ? c[i][j] : *acc + c[i][j];
-            if (last) store_elem((T*)a.ghidden + (int64_t)n * a.ghstride, d, has_target(a, n) ? s : 0.0f);
-            else *acc = s;
+// A piece's G.  bf16: rounded to nearest, an error of half a step of each
+// element where the products' sums are of thousands; fp32: three planes.
+template <typename Tile>
+__global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
+    __shared__ __align__(1024) char s0[Tile::Stage];
+    __shared__ __align__(1024) char s1[Tile::Stage];
+    constexpr int PL = Tile::PL;
+    const int count = *a.ws.count;
+    int im, in;
+    tile_of(blockIdx.x, tiles_of(nv, Tile::BM), tiles_of(a.N, Tile::BN), im, in);
+    const int m0 = im * Tile::BM, n0 = in * Tile::BN;
+    if (n0 >= count) return;
+    f32x4v acc[Tile::FM][Tile::FN] = {};
+    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, s0, s1, acc);
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
+    const int vl = rm + (lane >> 4) * 8;
+    const int64_t plane = rows_cap * a.plan.Vg;
+#pragma unroll
+    for (int j = 0; j < Tile::FN; ++j) {
+        const int n = rn + j * 16 + (lane & 15);
+        if (n >= count) continue;
+        const int t = a.ws.target[n] - vp - vl;
+        const float g = a.ws.gscale[n], lse = a.ws.lse[n];
+#pragma unroll
+        for (int i = 0; i < Tile::FM; i += 2) {
+            union {
+                uint16_t h[PL][8];
+                u32x4 v[PL];
+            } out;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int o = (i >> 1) * 32 + e;
+                const float z = acc[i + (e >> 2)][j][e & 3] * a.scale - lse;
+                float p = PL == 1 ? ex2(z * kLog2e) : expf(z);
+                if (o == t) p -= 1.0f;
+                uint16_t b[PL];
+                split_planes<PL>(vl + o < nv ? g * p : 0.0f, b);
+#pragma unroll
+                for (int pl = 0; pl < PL; ++pl) out.h[pl][e] = b[pl];
+            }
+            // the buffer's rows hold whole tiles: words behind the piece are zero
+            uint16_t* dst = a.ws.G + (int64_t)n * a.plan.Vg + vl + (i >> 1) * 32;
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) *(u32x4*)(dst + pl * plane) = out.v[pl];
         }
+    }
 }
 
-// grad_weight[v][d] = sum_n G[n][v] H[n][d]
-template <typename T>
-__global__ __launch_bounds__(256) void head_gweight_kernel(HeadArgs a, int vp, int nv) {
-    const int d0 = blockIdx.x * kT, v0 = blockIdx.y * kT;
-    float c[4][4];
-    tile_product(
-        a.N,
-        [&](int r, int k) {
-            return d0 + r < a.D && has_target(a, k) ? load_elem((const T*)a.hidden + (int64_t)k * a.hstride, d0 + r) : 0.0f;
-        },
-        [&](int r, int k) { return v0 + r < nv ? a.G[(int64_t)k * a.Vp + v0 + r] : 0.0f; }, c);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int j = 0; j < 4; ++j)
-        for (int i = 0; i < 4; ++i) {
-            const int v = v0 + tx * 4 + j, d = d0 + ty * 4 + i;
-            if (v >= nv || d >= a.D) continue;
-            T* o = (T*)a.gweight + (int64_t)(vp + v) * a.gwstride;
-            store_elem(o, d, a.accumulate ? load_elem(o, d) + c[i][j] : c[i][j]);
+// ------------------------------------------------------------- gradients
+
+// Partial sums of grad_hidden: split s of the piece's words, added to what the
+// pieces before left.
+template <typename Tile>
+__global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Operand W, int64_t rows_cap, int nv, int splits,
+                                                                bool first) {
+    __shared__ __align__(1024) char s0[Tile::Stage];
+    __shared__ __align__(1024) char s1[Tile::Stage];
+    const int count = *a.ws.count;
+    const int tm = tiles_of(a.D, Tile::BM), tn = tiles_of(a.N, Tile::BN);
+    const int s = blockIdx.x / (tm * tn);
+    int im, in;
+    tile_of(blockIdx.x % (tm * tn), tm, tn, im, in);
+    const int m0 = im * Tile::BM, n0 = in * Tile::BN;
+    if (n0 >= count) return;
+    const int per = tiles_of(tiles_of(nv, Tile::BK), splits) * Tile::BK;
+    const int k0 = s * per, k1 = min(nv, k0 + per);
+    f32x4v acc[Tile::FM][Tile::FN] = {};
+    // k behind the piece: G's words there are zero up to its row's end
+    Tile::run(W, m0, grad_operand(a, rows_cap, count), n0, k0, k1, s0, s1, acc);
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
+    float* gh = a.ws.gh + (int64_t)s * a.N * a.plan.Dp;
+#pragma unroll
+    for (int j = 0; j < Tile::FN; ++j) {
+        const int n = rn + j * 16 + (lane & 15);
+        if (n >= count) continue;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int d = rm + i * 16 + (lane >> 4) * 4;
+            if (d >= a.plan.Dp) continue;
+            f32x4v* o = (f32x4v*)(gh + (int64_t)n * a.plan.Dp + d);
+            *o = first ? acc[i][j] : *o + acc[i][j];
         }
+    }
 }
 
-unsigned tiles_of(int x) { return (unsigned)((x + kT - 1) / kT); }
+// grad_hidden: the splits' sums in order, one rounding; zero without a target.
+template <typename T>
+__global__ __launch_bounds__(256) void head_ghidden_out_kernel(HeadArgs a, int splits) {
+    const int n = blockIdx.x;
+    const int at = a.ws.place[n];
+    const int64_t stride = (int64_t)a.N * a.plan.Dp;
+    for (int d = threadIdx.x; d < a.D; d += 256) {
+        float s = 0.0f;
+        if (at >= 0)
+            for (int q = 0; q < splits; ++q) s += a.ws.gh[q * stride + (int64_t)at * a.plan.Dp + d];
+        store_elem((T*)a.ghidden + (int64_t)n * a.ghstride, d, s);
+    }
+}
 
 template <typename T>
-hipError_t head_loss_t(const HeadArgs& a, hipStream_t st) {
-    head_parts_kernel<T><<<dim3(tiles_of(a.V), tiles_of(a.N)), 256, 0, st>>>(a);
-    head_join_kernel<<<dim3((unsigned)((a.N + 255) / 256)), 256, 0, st>>>(a, (int)tiles_of(a.V));
+__device__ __forceinline__ void put_gweight(const HeadArgs& a, int64_t v, int d, f32x4v x) {
+    T* o = (T*)a.gweight + v * a.gwstride + d;
+    for (int r = 0; r < 4; ++r)
+        if (d + r < a.D) store_elem(o, r, a.accumulate ? load_elem(o, r) + x[r] : x[r]);
+}
+
+// The piece's rows of grad_weight, or (splits > 1) partial sums of them over a
+// split of the packed rows.
+template <typename T, typename Tile>
+__global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int64_t rows_cap, int vp, int nv, int splits) {
+    __shared__ __align__(1024) char s0[Tile::Stage];
+    __shared__ __align__(1024) char s1[Tile::Stage];
+    const int count = *a.ws.count;
+    const int tm = tiles_of(a.D, Tile::BM), tn = tiles_of(nv, Tile::BN);
+    const int s = blockIdx.x / (tm * tn);
+    int im, in;
+    tile_of(blockIdx.x % (tm * tn), tm, tn, im, in);
+    const int m0 = im * Tile::BM, n0 = in * Tile::BN;
+    const int per = tiles_of(tiles_of(count, Tile::BK), splits) * Tile::BK;
+    const int k0 = s * per, k1 = min(count, k0 + per);
+    f32x4v acc[Tile::FM][Tile::FN] = {};
+    Tile::run(hidden_operand(a, rows_cap, count), m0, grad_operand(a, rows_cap, count), n0, k0, k1, s0, s1, acc);
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
+#pragma unroll
+    for (int j = 0; j < Tile::FN; ++j) {
+        const int v = rn + j * 16 + (lane & 15);
+        if (v >= nv) continue;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int d = rm + i * 16 + (lane >> 4) * 4;
+            if (d >= a.plan.Dp) continue;
+            if (splits > 1) *(f32x4v*)(a.ws.gw + ((int64_t)s * nv + v) * a.plan.Dp + d) = acc[i][j];
+            else put_gweight<T>(a, vp + v, d, acc[i][j]);
+        }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void head_gweight_out_kernel(HeadArgs a, int vp, int nv, int splits) {
+    const int v = blockIdx.x;
+    for (int d = threadIdx.x * 4; d < a.D; d += 1024) {
+        f32x4v s = {};
+        for (int q = 0; q < splits; ++q) s += *(const f32x4v*)(a.ws.gw + ((int64_t)q * nv + v) * a.plan.Dp + d);
+        put_gweight<T>(a, vp + v, d, s);
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void head_zero_kernel(HeadArgs a) {
+    for (int d = threadIdx.x; d < a.D; d += 256) store_elem((T*)a.gweight + (int64_t)blockIdx.x * a.gwstride, d, 0.0f);
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int kMaxSplits = 64;
+constexpr int kFillTiles = 256;  // one tile to a CU
+
+// Splits of the k axis that bring `tiles` workgroups up to about one per CU, at
+// least four k steps each.
+int pick_splits(int tiles, int ksteps) {
+    int s = kFillTiles / (tiles > 0 ? tiles : 1);
+    if (s > ksteps / 4) s = ksteps / 4;
+    if (s > kMaxSplits) s = kMaxSplits;
+    return s < 1 ? 1 : s;
+}
+
+constexpr int64_t kPieceElems = 128ll << 20;   // of the logits' gradient
+constexpr int64_t kTableElems = 64ll << 20;    // of a packed piece of the table
+constexpr int64_t kPartRows = 65536;           // rows of a forward pass
+constexpr int kWordTile = 256;                 // pieces are whole tiles of any shape
+
+template <typename T>
+struct Planes {
+    static constexpr int value = sizeof(T) == 2 ? 1 : 3;
+};
+
+// Whether rows of 16-bit elements can be read as they lie: whole 16-byte
+// chunks, and offsets within a tile that fit 32 bits.
+bool reads_in_place(const void* p, int64_t stride, int D, int dtype) {
+    return dtype == GR_BF16 && D % 8 == 0 && stride % 8 == 0 && stride <= kMaxTileStride && (uintptr_t)p % 16 == 0;
+}
+
+bool use_large(int64_t m, int64_t n, int bm, int bn) { return (int64_t)tiles_of(m, bm) * tiles_of(n, bn) >= 192; }
+
+template <typename T>
+hipError_t pack_rows(const HeadArgs& a, int64_t cap, hipStream_t st) {
+    int per = kPackRows;
+    while (tiles_of(a.N, per) > 4096) per *= 2;  // the count before a workgroup's rows is quadratic in their number
+    pack_rows_kernel<T, Planes<T>::value><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per);
     return hipGetLastError();
 }
 
+// The operand of words [v, v + nv), packed first where it cannot be read in place.
 template <typename T>
-hipError_t head_backward_t(const HeadArgs& a, hipStream_t st) {
-    for (int vp = 0; vp < a.V; vp += a.Vp) {
-        const int nv = a.V - vp < a.Vp ? a.V - vp : a.Vp;
-        if (a.N) head_logit_grad_kernel<T><<<dim3(tiles_of(nv), tiles_of(a.N)), 256, 0, st>>>(a, vp);
-        if (a.N && a.ghidden)
-            head_ghidden_kernel<T><<<dim3(tiles_of(a.D), tiles_of(a.N)), 256, 0, st>>>(a, vp, nv, vp == 0, vp + nv == a.V);
-        if (a.gweight) head_gweight_kernel<T><<<dim3(tiles_of(a.D), tiles_of(nv)), 256, 0, st>>>(a, vp, nv);
+Operand words_operand(const HeadArgs& a, int v, int nv, int dtype, hipStream_t st) {
+    const int Dp = a.plan.Dp;
+    if (reads_in_place(a.weight, a.wstride, a.D, dtype)) {
+        const uint16_t* p = (const uint16_t*)a.weight + (int64_t)v * a.wstride;
+        return Operand{p, a.wstride, 0, (int64_t)(nv - 1) * a.wstride + a.D};
     }
+    pack_words_kernel<T, Planes<T>::value><<<dim3((unsigned)tiles_of(nv, 4)), 256, 0, st>>>(a, v, nv);
+    return Operand{a.ws.W, Dp, (int64_t)a.plan.Vw * Dp, (int64_t)nv * Dp};
+}
+
+template <typename Tile>
+void run_parts(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, hipStream_t st) {
+    head_parts_kernel<Tile><<<dim3((unsigned)(tiles_of(nv, Tile::BM) * tiles_of(a.N, Tile::BN))), Tile::NT, 0, st>>>(a, W, cap, v, nv);
+}
+
+template <typename T>
+hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
+    typedef typename TileFor<T, false, false, true>::type Large;
+    typedef typename TileFor<T, false, false, false>::type Small;
+    const int64_t cap = all.plan.part_rows;
+    for (int64_t r = 0; r < all.N; r += cap) {
+        HeadArgs a = all;
+        a.N = (int32_t)(all.N - r < cap ? all.N - r : cap);
+        a.hidden = (const T*)all.hidden + r * all.hstride;
+        a.targets = all.targets + r;
+        a.loss = all.loss + r;
+        a.lse = all.lse + r;
+        a.grad_loss = nullptr;
+        hipError_t e = pack_rows<T>(a, cap, st);
+        if (e != hipSuccess) return e;
+        const bool large = use_large(a.V, a.N, Large::BM, Large::BN);
+        const int step = reads_in_place(a.weight, a.wstride, a.D, dtype) ? a.V : a.plan.Vw;
+        for (int v = 0; v < a.V; v += step) {
+            const int nv = a.V - v < step ? a.V - v : step;
+            const Operand W = words_operand<T>(a, v, nv, dtype, st);
+            if (large) run_parts<Large>(a, W, cap, v, nv, st);
+            else run_parts<Small>(a, W, cap, v, nv, st);
+        }
+        const int parts = tiles_of(a.V, large ? Large::WM : Small::WM);
+        const int rb = a.N <= 64 ? 1 : 16;
+        head_join_kernel<<<dim3((unsigned)tiles_of(a.N, rb)), 1024, 0, st>>>(a, cap, parts, rb);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <typename Tile>
+void run_grad(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, hipStream_t st) {
+    head_grad_kernel<Tile><<<dim3((unsigned)(tiles_of(nv, Tile::BM) * tiles_of(a.N, Tile::BN))), Tile::NT, 0, st>>>(a, W, cap, v, nv);
+}
+
+template <typename Tile>
+int run_ghidden(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, hipStream_t st) {
+    const int tiles = tiles_of(a.D, Tile::BM) * tiles_of(a.N, Tile::BN);
+    // the first piece is the largest: its splits serve all
+    const int splits = pick_splits(tiles, tiles_of(a.V < a.plan.Vg ? a.V : a.plan.Vg, Tile::BK));
+    head_ghidden_kernel<Tile><<<dim3((unsigned)(tiles * splits)), Tile::NT, 0, st>>>(a, W, cap, nv, splits, v == 0);
+    return splits;
+}
+
+template <typename T, typename Tile>
+void run_gweight(const HeadArgs& a, int64_t cap, int v, int nv, hipStream_t st) {
+    const int tiles = tiles_of(a.D, Tile::BM) * tiles_of(nv, Tile::BN);
+    const int splits = pick_splits(tiles, tiles_of(a.N, Tile::BK));
+    head_gweight_kernel<T, Tile><<<dim3((unsigned)(tiles * splits)), Tile::NT, 0, st>>>(a, cap, v, nv, splits);
+    if (splits > 1) head_gweight_out_kernel<T><<<dim3((unsigned)nv), 256, 0, st>>>(a, v, nv, splits);
+}
+
+template <typename T>
+hipError_t head_backward_t(const HeadArgs& a, int dtype, hipStream_t st) {
+    typedef typename TileFor<T, false, false, true>::type ZLarge;
+    typedef typename TileFor<T, false, false, false>::type ZSmall;
+    typedef typename TileFor<T, true, false, true>::type HLarge;
+    typedef typename TileFor<T, true, false, false>::type HSmall;
+    typedef typename TileFor<T, true, true, true>::type WLarge;
+    typedef typename TileFor<T, true, true, false>::type WSmall;
+    const int64_t cap = a.plan.packed;
+    const hipError_t e = pack_rows<T>(a, cap, st);
+    if (e != hipSuccess) return e;
+    int splits = 1;
+    const bool in_place = reads_in_place(a.weight, a.wstride, a.D, dtype);
+    const int step = in_place || a.plan.Vg < a.plan.Vw ? a.plan.Vg : a.plan.Vw;
+    for (int v = 0; v < a.V; v += step) {
+        const int nv = a.V - v < step ? a.V - v : step;
+        const Operand W = words_operand<T>(a, v, nv, dtype, st);
+        if (use_large(nv, a.N, ZLarge::BM, ZLarge::BN)) run_grad<ZLarge>(a, W, cap, v, nv, st);
+        else run_grad<ZSmall>(a, W, cap, v, nv, st);
+        if (a.ghidden) {
+            if (use_large(a.D, a.N, HLarge::BM, HLarge::BN)) splits = run_ghidden<HLarge>(a, W, cap, v, nv, st);
+            else splits = run_ghidden<HSmall>(a, W, cap, v, nv, st);
+        }
+        if (a.gweight) {
+            if (use_large(a.D, nv, WLarge::BM, WLarge::BN)) run_gweight<T, WLarge>(a, cap, v, nv, st);
+            else run_gweight<T, WSmall>(a, cap, v, nv, st);
+        }
+    }
+    if (a.ghidden) head_ghidden_out_kernel<T><<<dim3((unsigned)a.N), 256, 0, st>>>(a, splits);
     return hipGetLastError();
 }
 
 }  // namespace
 
+HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool backward) {
+    const auto round_up = [](int64_t x, int64_t to) { return (x + to - 1) / to * to; };
+    HeadPlan p{};
+    p.planes = dtype == GR_BF16 ? 1 : 3;
+    p.Dp = (int32_t)round_up(dim, 8);
+    p.part_rows = (int32_t)(max_rows < kPartRows ? max_rows : kPartRows);
+    p.packed = backward ? max_rows : p.part_rows;
+    const int64_t words = round_up(vocab, kWordTile);
+    const int64_t vw = kTableElems / p.planes / p.Dp / kWordTile * kWordTile;
+    p.Vw = (int32_t)(vw < kWordTile ? kWordTile : (vw < words ? vw : words));
+    p.W = (int64_t)p.planes * p.Vw * p.Dp;
+    p.parts = (vocab + 63) / 64 * (int64_t)p.part_rows;  // the narrowest wave: 64 words
+    if (backward) {
+        const int64_t vg = kPieceElems / p.planes / max_rows / kWordTile * kWordTile;
+        p.Vg = (int32_t)(vg < kWordTile ? kWordTile : (vg < words ? vg : words));
+        p.G = (int64_t)p.planes * max_rows * p.Vg;
+        // a split product has at most kFillTiles tiles in all (pick_splits)
+        const int64_t most = (int64_t)kFillTiles * 256 * 256;
+        const int64_t h = max_rows * p.Dp, w = (int64_t)p.Vg * p.Dp;
+        p.gh = h > most ? h : (h * kMaxSplits < most ? h * kMaxSplits : most);
+        p.gw = w * kMaxSplits < most ? w * kMaxSplits : most;
+    }
+    return p;
+}
+
 hipError_t launch_head_loss(const HeadArgs& a, int dtype, hipStream_t st) {
     if (a.N == 0) return hipSuccess;
-    return dtype == GR_BF16 ? head_loss_t<uint16_t>(a, st) : head_loss_t<float>(a, st);
+    return dtype == GR_BF16 ? head_loss_t<uint16_t>(a, dtype, st) : head_loss_t<float>(a, dtype, st);
 }
 
 hipError_t launch_head_backward(const HeadArgs& a, int dtype, hipStream_t st) {
-    if (a.N == 0 && (a.accumulate || !a.gweight)) return hipSuccess;
-    return dtype == GR_BF16 ? head_backward_t<uint16_t>(a, st) : head_backward_t<float>(a, st);
+    if (a.N == 0) {
+        if (a.accumulate || !a.gweight) return hipSuccess;
+        if (dtype == GR_BF16) head_zero_kernel<uint16_t><<<dim3((unsigned)a.V), 256, 0, st>>>(a);
+        else head_zero_kernel<float><<<dim3((unsigned)a.V), 256, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    return dtype == GR_BF16 ? head_backward_t<uint16_t>(a, dtype, st) : head_backward_t<float>(a, dtype, st);
 }
 
 }  // namespace gr

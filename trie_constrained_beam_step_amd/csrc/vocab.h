@@ -28,7 +28,34 @@ struct EmbedBackwardArgs {
     int32_t accumulate;
 };
 
-// The head's workspace: what a handle of `max_rows` rows needs.
+// Sizes of a head's workspace, fixed at init for its most rows.
+struct HeadPlan {
+    int32_t planes;    // bf16 planes of an element: 1 (bf16) or 3 (fp32)
+    int32_t Dp;        // dim rounded up to 8
+    int32_t part_rows; // rows of one forward pass (more go in several)
+    int32_t Vg;        // words of a piece of the backward
+    int32_t Vw;        // words of a packed piece of the table
+    int64_t packed, parts, G, gh, gw, W;  // elements of the buffers below
+};
+
+HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool backward);
+
+// The workspace (device): rows that have a target are packed, in order.
+struct HeadSpace {
+    int32_t* count;    // [1] rows with a target
+    int32_t* target;   // [packed row] its target
+    int32_t* place;    // [row] its packed row, -1 without a target
+    float* gscale;     // [packed row] scale * grad_loss
+    float* lse;        // [packed row]
+    float* zt;         // [packed row] the target's logit
+    uint16_t* H;       // [planes][rows][Dp] packed hidden states
+    float2* parts;     // [parts of the vocabulary][rows] max and sum of exp(z - max)
+    uint16_t* W;       // [planes][Vw][Dp] a piece of the table, where it cannot be read as it lies
+    uint16_t* G;       // [planes][rows][Vg] a piece of the logits' gradient
+    float* gh;         // [splits][rows][Dp] partial sums of grad_hidden
+    float* gw;         // [splits][Vg][Dp] partial sums of grad_weight
+};
+
 struct HeadArgs {
     int32_t N, V, D;
     float scale;
@@ -38,22 +65,17 @@ struct HeadArgs {
     int64_t wstride;
     const int32_t* targets;  // [N]
     float* loss;             // [N] out
-    float* lse;              // [N] out (forward) / in (backward)
+    float* lse;              // [N] out
+    const float* lse_in;     // [N] in (backward)
     const float* grad_loss;  // [N]
     void* ghidden;           // [N] rows, ghstride apart, or nullptr
     int64_t ghstride;
     void* gweight;           // [V] rows, gwstride apart, or nullptr
     int64_t gwstride;
     int32_t accumulate;
-    // workspace
-    float2* parts;   // [tiles][N] max and sum of exp(z - max) of a row's tile
-    float* zt;       // [N] the target's logit
-    float* G;        // [N][Vp] a piece of the logits' gradient
-    int32_t Vp;      // words of a piece
-    float* gh_acc;   // [N][D] sums of grad_hidden over the pieces
+    HeadPlan plan;
+    HeadSpace ws;
 };
-
-constexpr int kHeadTile = 64;
 
 hipError_t launch_embed_lookup(const EmbedLookupArgs& a, int dtype, hipStream_t st);
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, int dtype, hipStream_t st);

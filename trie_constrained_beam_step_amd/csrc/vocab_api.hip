@@ -14,8 +14,6 @@ namespace {
 
 constexpr int32_t kMaxVocab = 1 << 30, kMaxDim = 65536, kMaxTokens = 1 << 24, kMaxRows = 1 << 20;
 constexpr int64_t kMaxStride = 1 << 22;
-// a piece of the logits' gradient holds at most so many elements
-constexpr int64_t kPieceElems = 64ll << 20;
 
 // Makes the handle's device current for a call and restores the caller's.
 struct OnDevice {
@@ -79,11 +77,8 @@ struct gr_embed {
 struct gr_head {
     gr_head_config cfg{};
     int device = 0;
-    int32_t Vp = 0;
-    float2* parts = nullptr;
-    float* zt = nullptr;
-    float* G = nullptr;
-    float* gh_acc = nullptr;
+    gr::HeadPlan plan{};
+    gr::HeadSpace ws{};
 };
 
 #define GR_TRY(expr)                          \
@@ -174,10 +169,9 @@ extern "C" void gr_embed_free(gr_embed* h) {
 // ------------------------------------------------------------------ head
 
 static void head_release(gr_head* h) {
-    (void)hipFree(h->parts);
-    (void)hipFree(h->zt);
-    (void)hipFree(h->G);
-    (void)hipFree(h->gh_acc);
+    const gr::HeadSpace& w = h->ws;
+    void* all[] = {w.count, w.target, w.place, w.gscale, w.lse, w.zt, w.H, w.parts, w.W, w.G, w.gh, w.gw};
+    for (void* p : all) (void)hipFree(p);
     delete h;
 }
 
@@ -193,15 +187,22 @@ extern "C" gr_status gr_head_init(const gr_head_config* cfg, gr_stream stream, g
     h->cfg = *cfg;
     h->device = dev;
     (void)stream;
-    const size_t N = cfg->max_rows, V = cfg->vocab, D = cfg->dim;
-    hipError_t e = dalloc(&h->parts, (V + gr::kHeadTile - 1) / gr::kHeadTile * N);
-    if (e == hipSuccess) e = dalloc(&h->zt, N);
+    const gr::HeadPlan p = gr::head_plan(cfg->max_rows, cfg->vocab, cfg->dim, cfg->dtype, !cfg->score_only);
+    h->plan = p;
+    gr::HeadSpace& w = h->ws;
+    hipError_t e = dalloc(&w.count, 1);
+    if (e == hipSuccess) e = dalloc(&w.target, p.packed);
+    if (e == hipSuccess) e = dalloc(&w.place, p.packed);
+    if (e == hipSuccess) e = dalloc(&w.zt, p.packed);
+    if (e == hipSuccess) e = dalloc(&w.H, (size_t)p.planes * p.packed * p.Dp);
+    if (e == hipSuccess) e = dalloc(&w.parts, p.parts);
+    if (e == hipSuccess) e = dalloc(&w.W, p.W);
     if (!cfg->score_only) {
-        int64_t vp = kPieceElems / (int64_t)N / gr::kHeadTile * gr::kHeadTile;
-        if (vp < gr::kHeadTile) vp = gr::kHeadTile;
-        h->Vp = vp > (int64_t)V ? (int32_t)V : (int32_t)vp;
-        if (e == hipSuccess) e = dalloc(&h->G, N * (size_t)h->Vp);
-        if (e == hipSuccess) e = dalloc(&h->gh_acc, N * D);
+        if (e == hipSuccess) e = dalloc(&w.gscale, p.packed);
+        if (e == hipSuccess) e = dalloc(&w.lse, p.packed);
+        if (e == hipSuccess) e = dalloc(&w.G, p.G);
+        if (e == hipSuccess) e = dalloc(&w.gh, p.gh);
+        if (e == hipSuccess) e = dalloc(&w.gw, p.gw);
     }
     if (e != hipSuccess) {
         head_release(h);
@@ -217,11 +218,8 @@ static gr::HeadArgs head_args(const gr_head* h, int32_t n) {
     a.V = h->cfg.vocab;
     a.D = h->cfg.dim;
     a.scale = h->cfg.scale;
-    a.parts = h->parts;
-    a.zt = h->zt;
-    a.G = h->G;
-    a.Vp = h->Vp;
-    a.gh_acc = h->gh_acc;
+    a.plan = h->plan;
+    a.ws = h->ws;
     return a;
 }
 
@@ -275,7 +273,7 @@ extern "C" gr_status gr_head_backward(gr_head* h, const void* d_hidden, int64_t 
     a.weight = d_weight;
     a.wstride = weight_row_stride;
     a.targets = d_targets;
-    a.lse = const_cast<float*>(d_lse);
+    a.lse_in = d_lse;
     a.grad_loss = d_grad_loss;
     a.ghidden = d_grad_hidden;
     a.ghstride = grad_hidden_row_stride;
