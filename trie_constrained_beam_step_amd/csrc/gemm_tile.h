@@ -76,39 +76,50 @@ struct GemmTile {
     static constexpr int ABytes = BM * BK * 2, BBytes = BN * BK * 2;  // a plane's
     static constexpr int Stage = PL * (ABytes + BBytes);
 
-    // Copies one operand's R x BK tile (all planes) into LDS.  `base` is the
-    // tile's first element, `rem` the bytes from there to the operand's end,
-    // kleft the k elements left.
+    // Copies one operand's R x BK tile (all planes) into LDS, one k step after
+    // the other.
     template <int R, bool Across, bool Perm>
-    static __device__ __forceinline__ void fetch(char* lds, const uint16_t* base, int64_t ld, int64_t plane, int64_t rem,
-                                                 int kleft) {
-        constexpr int kRowChunks = Across ? R / 8 : BK / 8;
-        constexpr int kRowsPerRound = NT / kRowChunks;
-        constexpr int kRounds = R * BK * 2 / (NT * 16);
+    struct Fetch {
+        static constexpr int kRowChunks = Across ? R / 8 : BK / 8;
+        static constexpr int kRowsPerRound = NT / kRowChunks;
+        static constexpr int kRounds = R * BK * 2 / (NT * 16);
         static_assert(R * BK * 2 % (NT * 16) == 0, "whole rounds");
         static_assert(kRowsPerRound % 16 == 0, "the swizzle repeats from round to round");
-        const int tid = threadIdx.x;
-        const int row = tid / kRowChunks, c = tid % kRowChunks;
-        uint32_t off;
-        if (Across) {
-            off = (uint32_t)row * (uint32_t)(ld * 2) + (uint32_t)(c ^ (across_swz(row) << 1)) * 16u;
-        } else {
-            const int src = c ^ along_swz<kRowChunks, Perm>(row);
-            off = (uint32_t)row * (uint32_t)(ld * 2) + (uint32_t)src * 16u;
-            if (src * 8 >= kleft) off = 0x80000000u;  // behind the last k: zero
+        const char* base;  // the next step's first element
+        int64_t rem;       // bytes from there to the operand's end
+        int64_t plane, advance;
+        uint32_t off, step;
+        int kfirst;        // "along": this lane's first k in a step
+
+        __device__ __forceinline__ Fetch(const Operand& o, int64_t r0, int64_t k0) {
+            const int row = threadIdx.x / kRowChunks, c = threadIdx.x % kRowChunks;
+            const int src = Across ? c ^ (across_swz(row) << 1) : c ^ along_swz<kRowChunks, Perm>(row);
+            const int64_t first = Across ? k0 * o.ld + r0 : r0 * o.ld + k0;
+            base = (const char*)(o.p + first);
+            rem = (o.n - first) * 2;
+            plane = o.plane * 2;
+            advance = (Across ? o.ld : 1) * BK * 2;
+            off = (uint32_t)row * (uint32_t)(o.ld * 2) + (uint32_t)src * 16u;
+            step = (uint32_t)kRowsPerRound * (uint32_t)(o.ld * 2);
+            kfirst = Across ? 0 : src * 8;
         }
-        const uint32_t step = (uint32_t)kRowsPerRound * (uint32_t)(ld * 2);
-        const uint32_t n = rem > 0x7FFFFFFF ? 0x7FFFFFFFu : (rem > 0 ? (uint32_t)rem : 0u);
-        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+        // kleft: the k elements left from this step on.  `wave_lds`: the stage's
+        // place for this operand, plus the wave's 1 KB.
+        __device__ __forceinline__ void operator()(char* wave_lds, int kleft) {
+            const uint32_t n = rem > 0x7FFFFFFF ? 0x7FFFFFFFu : (rem > 0 ? (uint32_t)rem : 0u);
+            uint32_t o = Across || kfirst < kleft ? off : 0x80000000u;  // behind the last k: zero
 #pragma unroll
-        for (int pl = 0; pl < PL; ++pl) {
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)(base + pl * plane), 0, n, kBufferFlags);
+            for (int r = 0; r < kRounds; ++r, o += step)
 #pragma unroll
-            for (int r = 0; r < kRounds; ++r)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rsrc, (lds_void*)(lds + pl * R * BK * 2 + r * NT * 16 + wave * 1024), 16, off + r * step, 0, 0, 0);
+                for (int pl = 0; pl < PL; ++pl)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                        __builtin_amdgcn_make_buffer_rsrc((void*)(base + pl * plane), 0, n, kBufferFlags),
+                        (lds_void*)(wave_lds + pl * R * BK * 2 + r * NT * 16), 16, o, 0, 0, 0);
+            base += advance;
+            rem -= advance;
         }
-    }
+    };
 
     // Fragment (16 rows x 32 k) of an "along" tile.
     template <bool Perm>
@@ -131,35 +142,45 @@ struct GemmTile {
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 
+    // The fragments of step s (k half s / FM, A's fragment s % FM) are read two
+    // steps before their matrix instructions, and the half's B fragments with
+    // its first: the order is fixed, or the compiler reads a whole stage ahead
+    // and spills.
     static __device__ __forceinline__ void multiply(const char* lds, f32x4v (&acc)[FM][FN]) {
         const int wave = threadIdx.x >> 6;
         const int rm = (wave / (BN / WN)) * WM, rn = (wave % (BN / WN)) * WN;
-#pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) {
-            bf16x8 a[PL][FM], b[PL][FN];
+        constexpr int kSteps = BK / 32 * FM, kAhead = 2;
+        bf16x8 a[kAhead + 1][PL], b[2][PL][FN];
+        const auto read = [&](int s) {
+            const int kk = s / FM, i = s % FM;
 #pragma unroll
             for (int pl = 0; pl < PL; ++pl) {
+                if (i == 0)
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const char* s = lds + PL * ABytes + pl * BBytes;
-                    b[pl][j] = BAcross ? frag_across<BN>(s, rn, j, kk) : frag_along<false>(s, rn, j, kk);
-                }
-#pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    const char* s = lds + pl * ABytes;
-                    a[pl][i] = AAcross ? frag_across<BM>(s, rm, i, kk) : frag_along<kPerm>(s, rm, i, kk);
-                }
+                    for (int j = 0; j < FN; ++j) {
+                        const char* t = lds + PL * ABytes + pl * BBytes;
+                        b[kk & 1][pl][j] = BAcross ? frag_across<BN>(t, rn, j, kk) : frag_along<false>(t, rn, j, kk);
+                    }
+                const char* t = lds + pl * ABytes;
+                a[s % (kAhead + 1)][pl] = AAcross ? frag_across<BM>(t, rm, i, kk) : frag_along<kPerm>(t, rm, i, kk);
             }
-            // the small pairs first
+        };
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) read(s);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            if (s + kAhead < kSteps) read(s + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+            // the small pairs of planes first
 #pragma unroll
             for (int sum = PL - 1; sum >= 0; --sum)
 #pragma unroll
                 for (int pa = sum; pa >= 0; --pa)
 #pragma unroll
-                    for (int i = 0; i < FM; ++i)
-#pragma unroll
-                        for (int j = 0; j < FN; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[pa][i], b[sum - pa][j], acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < FN; ++j)
+                        acc[s % FM][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s % (kAhead + 1)][pa], b[(s / FM) & 1][sum - pa][j],
+                                                                                acc[s % FM][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
@@ -172,30 +193,29 @@ struct GemmTile {
         asm volatile("" ::: "memory");
     }
 
-    // acc += the tile at rows m0 of A and n0 of B, k in [k0, k1).  s0, s1: two
-    // stages of LDS.  k0 is a multiple of 8 and k1 of BK, or what lies behind
-    // k1 is zero in one operand and finite in the other (rows behind an
-    // "across" operand's end are zero).
-    static __device__ __forceinline__ void run(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int64_t k0,
-                                               int64_t k1, char* s0, char* s1, f32x4v (&acc)[FM][FN]) {
-        const auto load = [&](char* lds, int64_t k) {
-            const int kleft = (int)(k1 - k < BK ? k1 - k : BK);
-            const int64_t ao = AAcross ? k * A.ld + m0 : m0 * A.ld + k;
-            const int64_t bo = BAcross ? k * B.ld + n0 : n0 * B.ld + k;
-            fetch<BM, AAcross, kPerm>(lds, A.p + ao, A.ld, A.plane, (A.n - ao) * 2, kleft);
-            fetch<BN, BAcross, false>(lds + PL * ABytes, B.p + bo, B.ld, B.plane, (B.n - bo) * 2, kleft);
-        };
+    // acc += the tile at rows m0 of A and n0 of B, k in [k0, k1).  lds: two
+    // stages.  k0 is a multiple of 8 and k1 of BK, or what lies behind k1 is
+    // zero in one operand and finite in the other (rows behind an "across"
+    // operand's end are zero).
+    static __device__ __forceinline__ void run(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int k0, int k1,
+                                               char* lds, f32x4v (&acc)[FM][FN]) {
         if (k0 >= k1) return;
-        load(s0, k0);
+        Fetch<BM, AAcross, kPerm> fa(A, m0, k0);
+        Fetch<BN, BAcross, false> fb(B, n0, k0);
+        char* wave_lds = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+        fa(wave_lds, k1 - k0);
+        fb(wave_lds + PL * ABytes, k1 - k0);
         stage_barrier();
-        for (int64_t k = k0; k < k1; k += 2 * BK) {
-            if (k + BK < k1) load(s1, k + BK);
-            multiply(s0, acc);
+        int stage = 0;
+        for (int k = k0; k < k1; k += BK) {
+            const int next = Stage - stage;
+            if (k + BK < k1) {
+                fa(wave_lds + next, k1 - k - BK);
+                fb(wave_lds + next + PL * ABytes, k1 - k - BK);
+            }
+            multiply(lds + stage, acc);
             stage_barrier();
-            if (k + BK >= k1) break;
-            if (k + 2 * BK < k1) load(s0, k + 2 * BK);
-            multiply(s1, acc);
-            stage_barrier();
+            stage = next;
         }
     }
 };

@@ -166,15 +166,14 @@ __device__ __forceinline__ Operand grad_operand(const HeadArgs& a, int64_t rows_
 
 template <typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
-    __shared__ __align__(1024) char s0[Tile::Stage];
-    __shared__ __align__(1024) char s1[Tile::Stage];
+    __shared__ __align__(1024) char lds[2 * Tile::Stage];
     const int count = *a.ws.count;
     int im, in;
     tile_of(blockIdx.x, tiles_of(nv, Tile::BM), tiles_of(a.N, Tile::BN), im, in);
     const int m0 = im * Tile::BM, n0 = in * Tile::BN;
     if (n0 >= count) return;
     f32x4v acc[Tile::FM][Tile::FN] = {};
-    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, s0, s1, acc);
+    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, lds, acc);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
@@ -254,8 +253,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t row
 // element where the products' sums are of thousands; fp32: three planes.
 template <typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
-    __shared__ __align__(1024) char s0[Tile::Stage];
-    __shared__ __align__(1024) char s1[Tile::Stage];
+    __shared__ __align__(1024) char lds[2 * Tile::Stage];
     constexpr int PL = Tile::PL;
     const int count = *a.ws.count;
     int im, in;
@@ -263,7 +261,7 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
     const int m0 = im * Tile::BM, n0 = in * Tile::BN;
     if (n0 >= count) return;
     f32x4v acc[Tile::FM][Tile::FN] = {};
-    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, s0, s1, acc);
+    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, lds, acc);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
@@ -307,8 +305,7 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
 template <typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Operand W, int64_t rows_cap, int nv, int splits,
                                                                 bool first) {
-    __shared__ __align__(1024) char s0[Tile::Stage];
-    __shared__ __align__(1024) char s1[Tile::Stage];
+    __shared__ __align__(1024) char lds[2 * Tile::Stage];
     const int count = *a.ws.count;
     const int tm = tiles_of(a.D, Tile::BM), tn = tiles_of(a.N, Tile::BN);
     const int s = blockIdx.x / (tm * tn);
@@ -320,7 +317,7 @@ __global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Oper
     const int k0 = s * per, k1 = min(nv, k0 + per);
     f32x4v acc[Tile::FM][Tile::FN] = {};
     // k behind the piece: G's words there are zero up to its row's end
-    Tile::run(W, m0, grad_operand(a, rows_cap, count), n0, k0, k1, s0, s1, acc);
+    Tile::run(W, m0, grad_operand(a, rows_cap, count), n0, k0, k1, lds, acc);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
@@ -364,8 +361,7 @@ __device__ __forceinline__ void put_gweight(const HeadArgs& a, int64_t v, int d,
 // split of the packed rows.
 template <typename T, typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int64_t rows_cap, int vp, int nv, int splits) {
-    __shared__ __align__(1024) char s0[Tile::Stage];
-    __shared__ __align__(1024) char s1[Tile::Stage];
+    __shared__ __align__(1024) char lds[2 * Tile::Stage];
     const int count = *a.ws.count;
     const int tm = tiles_of(a.D, Tile::BM), tn = tiles_of(nv, Tile::BN);
     const int s = blockIdx.x / (tm * tn);
@@ -375,7 +371,7 @@ __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int6
     const int per = tiles_of(tiles_of(count, Tile::BK), splits) * Tile::BK;
     const int k0 = s * per, k1 = min(count, k0 + per);
     f32x4v acc[Tile::FM][Tile::FN] = {};
-    Tile::run(hidden_operand(a, rows_cap, count), m0, grad_operand(a, rows_cap, count), n0, k0, k1, s0, s1, acc);
+    Tile::run(hidden_operand(a, rows_cap, count), m0, grad_operand(a, rows_cap, count), n0, k0, k1, lds, acc);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
