@@ -177,6 +177,29 @@ def test_head(gr, dtype, n, vocab, dim):
     head.close()
 
 
+# shapes that fill the chip with large tiles: in the first product (words x
+# rows), in grad_hidden (width x rows) and in grad_weight (width x words); the
+# third has more rows than a piece of the vocabulary allows whole (several
+# pieces, the last of odd size)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab,dim", [(2300, 6100, 136), (6200, 333, 2048), (300, 6301, 2048), (40_000, 4000, 64)])
+def test_head_large(gr, dtype, n, vocab, dim):
+    """The 64-bit formulas run on the GPU here (torch's fp64 products)."""
+    h, w, t, g, (hc, gc) = (x if isinstance(x, tuple) else x.cuda() for x in _head_inputs(n, vocab, dim, dtype, 3 * n))
+    want = vu.head(hc.cuda(), w, t, 1.0, dtype, gc.cuda())
+    want = {k: v.cpu() for k, v in want.items()}
+    head = gr.Head(vocab, dim, max_rows=n, dtype=dtype)
+    loss, lse = head.loss(h, w, t)
+    vu.check("loss", loss, want["loss"], want["loss_err"])
+    vu.check("lse", lse, want["lse"], want["lse_err"])
+    gh, gw = head.backward(h, w, t, lse, g)
+    vu.check("grad_hidden", gh, want["gh"], want["gh_err"])
+    vu.check("grad_weight", gw, want["gw"], want["gw_err"])
+    again = head.backward(h, w, t, lse, g)
+    assert torch.equal(again[0], gh) and torch.equal(again[1], gw), "two calls differ"
+    head.close()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_head_fewer_rows_than_planned(gr, dtype):
     """One handle, calls of every size up to its most: each as a handle of its own."""

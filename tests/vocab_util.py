@@ -36,10 +36,10 @@ def head(hidden, weight, targets, scale, dtype, grad_loss=None, base=None):
     t = targets.flatten().long()
     ok = (t >= 0) & (t < V)
     h = torch.where(ok[:, None], hidden.reshape(-1, D).double(), 0.0)
-    w = weight.double()
+    w = weight.double().contiguous()
     at = torch.where(ok, t, 0)[:, None]
-    z = h @ w.T * scale
-    ez = (D + 8) * U * (h.abs() @ w.abs().T) * abs(scale)  # error of a logit
+    z = h @ w.T.contiguous() * scale
+    ez = (D + 8) * U * (h.abs() @ w.abs().T.contiguous()) * abs(scale)  # error of a logit
     ezr = ez.max(1).values
     lse = torch.logsumexp(z, 1)
     spread = (z.max(1).values[:, None] - z).clamp(max=100).max(1).values
@@ -57,7 +57,7 @@ def head(hidden, weight, targets, scale, dtype, grad_loss=None, base=None):
     g = torch.where(ok, grad_loss.flatten().double(), zero)[:, None] * scale
     p = torch.exp(z - lse[:, None])
     G = p.clone()
-    G[torch.arange(len(t)), at[:, 0]] -= 1.0
+    G[torch.arange(len(t), device=t.device), at[:, 0]] -= 1.0
     G = G * g
     # a probability is off by its exponent's error; G is rounded to the
     # element type (bf16) or held in fp32

@@ -44,20 +44,59 @@ __device__ __forceinline__ void split_planes(float x, uint16_t (&out)[PL]) {
 }
 
 __device__ __forceinline__ bool has_target(const HeadArgs& a, int n) {
-    return n < a.N && a.targets[n] >= 0 && a.targets[n] < a.V;
+    return n < a.N && (uint32_t)a.targets[n] < (uint32_t)a.V;
 }
 
 // ------------------------------------------------------------ packing
 
-// Row `src` of D elements into PL planes of Dp.
-template <typename T, int PL>
-__device__ __forceinline__ void pack_row(const T* src, int D, int Dp, uint16_t* dst, int64_t plane, int lane, int lanes) {
-    for (int d = lane; d < Dp; d += lanes) {
-        uint16_t b[PL];
-        split_planes<PL>(d < D ? load_elem(src, d) : 0.0f, b);
+// Elements [d, d + 8) of a row: 16-byte loads where `wide` (the row starts on 16
+// bytes), zeros behind D.
+__device__ __forceinline__ void load8(const float* src, int d, int D, bool wide, float (&x)[8]) {
+    if (wide && d + 8 <= D) {
+        const f32x4v lo = *(const f32x4v*)(src + d), hi = *(const f32x4v*)(src + d + 4);
 #pragma unroll
-        for (int p = 0; p < PL; ++p) dst[p * plane + d] = b[p];
+        for (int e = 0; e < 4; ++e) x[e] = lo[e], x[e + 4] = hi[e];
+        return;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = d + e < D ? src[d + e] : 0.0f;
+}
+__device__ __forceinline__ u32x4 load8_bits(const uint16_t* src, int d, int D, bool wide) {
+    if (wide && d + 8 <= D) return *(const u32x4*)(src + d);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (d + e < D) v[e >> 1] |= (uint32_t)src[d + e] << (16 * (e & 1));
+    return v;
+}
+
+// Row `src` of D elements into planes of Dp (a multiple of 8).
+__device__ __forceinline__ void pack_row(const uint16_t* src, int D, int Dp, bool wide, uint16_t* dst, int64_t, int lane,
+                                         int lanes) {
+    for (int d = lane * 8; d < Dp; d += lanes * 8) *(u32x4*)(dst + d) = load8_bits(src, d, D, wide);
+}
+__device__ __forceinline__ void pack_row(const float* src, int D, int Dp, bool wide, uint16_t* dst, int64_t plane, int lane,
+                                         int lanes) {
+    for (int d = lane * 8; d < Dp; d += lanes * 8) {
+        float x[8];
+        load8(src, d, D, wide, x);
+        u32x4 v[3] = {};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint16_t b[3];
+            split_planes<3>(x[e], b);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) v[p][e >> 1] |= (uint32_t)b[p] << (16 * (e & 1));
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *(u32x4*)(dst + p * plane + d) = v[p];
+    }
+}
+
+// Rows from `p` on, `stride` apart, all start on 16 bytes.
+template <typename T>
+__device__ __forceinline__ bool rows_wide(const T* p, int64_t stride) {
+    return (uintptr_t)p % 16 == 0 && stride % (16 / (int)sizeof(T)) == 0;
 }
 
 constexpr int kPackRows = 16;  // rows of a workgroup
@@ -65,12 +104,22 @@ constexpr int kPackRows = 16;  // rows of a workgroup
 // The rows that have a target, packed in order.  Each workgroup counts the
 // targets before its own rows by itself (the targets of 2^16 rows are 256 KB
 // of L2 reads; a scan kernel before this one would cost a launch).
-template <typename T, int PL>
+template <typename T>
 __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows_cap, int rows_per_wg) {
     __shared__ int wsum[4], base;
     const int r0 = blockIdx.x * rows_per_wg;
     int c = 0;
-    for (int i = threadIdx.x; i < r0; i += 256) c += has_target(a, i) ? 1 : 0;
+    if ((uintptr_t)a.targets % 16 == 0) {  // r0 is a multiple of 4
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll 4
+        for (int i = threadIdx.x * 4; i < r0; i += 1024) {
+            const i32x4 t = *(const i32x4*)(a.targets + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c += (uint32_t)t[e] < (uint32_t)a.V ? 1 : 0;
+        }
+    } else {
+        for (int i = threadIdx.x; i < r0; i += 256) c += (uint32_t)a.targets[i] < (uint32_t)a.V ? 1 : 0;
+    }
     c = (int)wave_sum_ll(c);
     if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = c;
     __syncthreads();
@@ -78,6 +127,7 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
     __syncthreads();
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int r2 = min(r0 + rows_per_wg, a.N);
+    const bool wide = rows_wide((const T*)a.hidden, a.hstride);
     int before = base;
     for (int r1 = r0; r1 < r2; r1 += 64) {
         const int mine = r1 + lane;
@@ -98,8 +148,8 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
         for (uint64_t rest = m; rest; rest &= rest - 1, ++k) {
             if ((k & 3) != wave) continue;
             const int row = r1 + __builtin_ctzll(rest);
-            pack_row<T, PL>((const T*)a.hidden + (int64_t)row * a.hstride, a.D, a.plan.Dp,
-                            a.ws.H + (int64_t)(before + k) * a.plan.Dp, rows_cap * a.plan.Dp, lane, 64);
+            pack_row((const T*)a.hidden + (int64_t)row * a.hstride, a.D, a.plan.Dp, wide,
+                     a.ws.H + (int64_t)(before + k) * a.plan.Dp, rows_cap * a.plan.Dp, lane, 64);
         }
         before += __popcll(m);
     }
@@ -107,12 +157,12 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
 }
 
 // Words [v0, v0 + nv) of the table in planes.
-template <typename T, int PL>
+template <typename T>
 __global__ __launch_bounds__(256) void pack_words_kernel(HeadArgs a, int v0, int nv) {
     const int v = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (v >= nv) return;
-    pack_row<T, PL>((const T*)a.weight + (int64_t)(v0 + v) * a.wstride, a.D, a.plan.Dp, a.ws.W + (int64_t)v * a.plan.Dp,
-                    (int64_t)a.plan.Vw * a.plan.Dp, threadIdx.x & 63, 64);
+    pack_row((const T*)a.weight + (int64_t)(v0 + v) * a.wstride, a.D, a.plan.Dp, rows_wide((const T*)a.weight, a.wstride),
+             a.ws.W + (int64_t)v * a.plan.Dp, (int64_t)a.plan.Vw * a.plan.Dp, threadIdx.x & 63, 64);
 }
 
 // ----------------------------------------------------------- tile order
@@ -423,11 +473,6 @@ constexpr int64_t kTableElems = 64ll << 20;    // of a packed piece of the table
 constexpr int64_t kPartRows = 65536;           // rows of a forward pass
 constexpr int kWordTile = 256;                 // pieces are whole tiles of any shape
 
-template <typename T>
-struct Planes {
-    static constexpr int value = sizeof(T) == 2 ? 1 : 3;
-};
-
 // Whether rows of 16-bit elements can be read as they lie: whole 16-byte
 // chunks, and offsets within a tile that fit 32 bits.
 bool reads_in_place(const void* p, int64_t stride, int D, int dtype) {
@@ -440,7 +485,7 @@ template <typename T>
 hipError_t pack_rows(const HeadArgs& a, int64_t cap, hipStream_t st) {
     int per = kPackRows;
     while (tiles_of(a.N, per) > 4096) per *= 2;  // the count before a workgroup's rows is quadratic in their number
-    pack_rows_kernel<T, Planes<T>::value><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per);
+    pack_rows_kernel<T><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per);
     return hipGetLastError();
 }
 
@@ -452,7 +497,7 @@ Operand words_operand(const HeadArgs& a, int v, int nv, int dtype, hipStream_t s
         const uint16_t* p = (const uint16_t*)a.weight + (int64_t)v * a.wstride;
         return Operand{p, a.wstride, 0, (int64_t)(nv - 1) * a.wstride + a.D};
     }
-    pack_words_kernel<T, Planes<T>::value><<<dim3((unsigned)tiles_of(nv, 4)), 256, 0, st>>>(a, v, nv);
+    pack_words_kernel<T><<<dim3((unsigned)tiles_of(nv, 4)), 256, 0, st>>>(a, v, nv);
     return Operand{a.ws.W, Dp, (int64_t)a.plan.Vw * Dp, (int64_t)nv * Dp};
 }
 
