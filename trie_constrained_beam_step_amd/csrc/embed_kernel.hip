@@ -1,5 +1,17 @@
 // embed_kernel.hip -- rows of the embedding table for a step's tokens, and the
 // table's gradient from those rows' gradient.
+//
+// Both move rows and add little: they are bound by HBM.  A row is read and
+// written 16 bytes a thread (one element a thread where the rows do not start
+// on 16 bytes), `lanes` threads to a row.
+//
+// The gradient has one writer per word and no floating-point atomics.  Few
+// tokens (embed_few_kernel): one launch, each workgroup collects its words'
+// tokens itself.  More: a stable radix sort of the token positions by word (its first
+// launch also fills the gradient with zeros), then every `tile` neighbours in
+// the sorted order are summed by one group of threads; a word that lies inside
+// one tile is written at once, the sums of one that crosses tiles are joined in
+// order by a last kernel.  The order of every sum depends on the tokens alone.
 #include "device_common.h"
 #include "gr.h"
 #include "vocab.h"
@@ -7,57 +19,459 @@
 namespace gr {
 namespace {
 
-__device__ __forceinline__ void store_elem(float* p, int64_t i, float v) { p[i] = v; }
-// bf16 with round to nearest even; NaN stays NaN
-__device__ __forceinline__ void store_elem(uint16_t* p, int64_t i, float v) {
-    const uint32_t b = __float_as_uint(v);
-    p[i] = (v != v) ? (uint16_t)((b >> 16) | 0x40) : (uint16_t)((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
-}
+typedef float f32x4v __attribute__((ext_vector_type(4)));
 
-template <typename T>
-__global__ __launch_bounds__(256) void embed_lookup_kernel(EmbedLookupArgs a) {
-    const int64_t i = blockIdx.x;
-    const int32_t t = a.tokens[i];
-    const bool ok = t >= 0 && t < a.V;
-    const T* w = (const T*)a.weight + (int64_t)(ok ? t : 0) * a.wstride;
-    T* o = (T*)a.out + i * a.ostride;
-    for (int d = threadIdx.x; d < a.D; d += 256) store_elem(o, d, ok ? load_elem(w, d) * a.scale : 0.0f);
-}
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// One workgroup per word walks all tokens.
+// N consecutive elements as fp32: 16 bytes of them, or one.
+template <typename T, int N>
+struct Pack;
 template <typename T>
-__global__ __launch_bounds__(256) void embed_backward_kernel(EmbedBackwardArgs a) {
-    const int32_t v = blockIdx.x;
-    T* o = (T*)a.gweight + (int64_t)v * a.wstride;
-    for (int d0 = 0; d0 < a.D; d0 += 256) {
-        const int d = d0 + threadIdx.x;
-        float acc = 0.0f;
-        bool any = false;
-        for (int i = 0; i < a.n; ++i) {
-            if (a.tokens[i] != v) continue;
-            any = true;
-            if (d < a.D) acc += load_elem((const T*)a.grad + (int64_t)i * a.gstride, d);
-        }
-        if (d >= a.D) continue;
-        if (!a.accumulate) store_elem(o, d, acc * a.scale);
-        else if (any) store_elem(o, d, fmaf(acc, a.scale, load_elem(o, d)));
+struct Pack<T, 1> {
+    static __device__ __forceinline__ void load(const T* p, float (&x)[1]) { x[0] = load_elem(p, 0); }
+    static __device__ __forceinline__ void store(float* p, const float (&x)[1]) { *p = x[0]; }
+    static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[1]) { *p = bf16_bits(x[0]); }
+};
+template <>
+struct Pack<float, 4> {
+    static __device__ __forceinline__ void load(const float* p, float (&x)[4]) {
+        const f32x4v v = *(const f32x4v*)p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = v[e];
     }
+    static __device__ __forceinline__ void store(float* p, const float (&x)[4]) { *(f32x4v*)p = f32x4v{x[0], x[1], x[2], x[3]}; }
+};
+template <>
+struct Pack<uint16_t, 8> {
+    static __device__ __forceinline__ void load(const uint16_t* p, float (&x)[8]) {
+        const u32x4 v = *(const u32x4*)p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(v[e] << 16);
+            x[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[8]) {
+        u32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = bf16_bits(x[2 * e]) | (uint32_t)bf16_bits(x[2 * e + 1]) << 16;
+        *(u32x4*)p = v;
+    }
+};
+
+// Writes a word's sum: scaled, or added to what its row holds.
+template <typename T, int N>
+__device__ __forceinline__ void put_word(const EmbedBackwardArgs& a, int v, int d, float (&s)[N]) {
+    T* o = (T*)a.gweight + (int64_t)v * a.wstride + d;
+    if (a.accumulate) {
+        float old[N];
+        Pack<T, N>::load(o, old);
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = fmaf(s[e], a.scale, old[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] *= a.scale;
+    }
+    Pack<T, N>::store(o, s);
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void add_row(const EmbedBackwardArgs& a, int i, int d, float (&s)[N]) {
+    float x[N];
+    Pack<T, N>::load((const T*)a.grad + (int64_t)i * a.gstride + d, x);
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e] += x[e];
+}
+
+constexpr int kFewWords = 512;  // words of an embed_few_kernel workgroup at most
+
+__device__ __forceinline__ bool in_table(int t, int V) { return (uint32_t)t < (uint32_t)V; }
+
+// --------------------------------------------------------------- lookup
+
+// 256 / lanes groups of `lanes` threads, each R rows at a time: their tokens,
+// then their elements, are loaded together.
+template <typename T, int N, int R>
+__global__ __launch_bounds__(256) void embed_lookup_kernel(EmbedLookupArgs a, int lanes) {
+    const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int64_t i0 = ((int64_t)blockIdx.x * (256 / lanes) + group) * R;
+    int t[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) t[r] = i0 + r < a.n ? a.tokens[i0 + r] : -1;
+    for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
+        float x[R][N];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[r][e] = 0.0f;
+            if (in_table(t[r], a.V)) Pack<T, N>::load((const T*)a.weight + (int64_t)t[r] * a.wstride + d, x[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (i0 + r >= a.n) break;
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[r][e] = in_table(t[r], a.V) ? x[r][e] * a.scale : 0.0f;
+            Pack<T, N>::store((T*)a.out + (i0 + r) * a.ostride + d, x[r]);
+        }
+    }
+}
+
+// ------------------------------------------------------- few tokens, one launch
+
+// A workgroup owns the words [x*words, (x+1)*words).  It lists the positions of
+// its words' tokens in order, ranks them by word (counting the better ones in
+// LDS: the list is short), and its groups of threads take the words in turn.
+template <typename T, int N>
+__global__ __launch_bounds__(256) void embed_few_kernel(EmbedBackwardArgs a, int lanes, int words) {
+    __shared__ int pos[kEmbedFew], word[kEmbedFew], sorted[kEmbedFew], wcount[4];
+    __shared__ int first[kFewWords], count[kFewWords];
+    const int v0 = blockIdx.x * words, nv = min(words, a.V - v0);
+    const int wave = threadIdx.x >> 6;
+    for (int v = threadIdx.x; v < nv; v += 256) count[v] = 0;
+    int m = 0;
+    for (int i0 = 0; i0 < a.n; i0 += 256) {
+        const int i = i0 + threadIdx.x;
+        const int t = i < a.n ? a.tokens[i] : -1;
+        const bool mine = t >= v0 && t < v0 + nv;
+        const uint64_t b = __ballot(mine);
+        if ((threadIdx.x & 63) == 0) wcount[wave] = __popcll(b);
+        __syncthreads();
+        int at = m + lanes_below(b);
+        for (int w = 0; w < wave; ++w) at += wcount[w];
+        if (mine) {
+            pos[at] = i;
+            word[at] = t - v0;
+        }
+        m += wcount[0] + wcount[1] + wcount[2] + wcount[3];
+        __syncthreads();
+    }
+    for (int q = threadIdx.x; q < m; q += 256) {
+        const int v = word[q];
+        int below = 0, same = 0;
+        for (int r = 0; r < m; ++r) {
+            below += word[r] < v ? 1 : 0;
+            same += word[r] == v && r < q ? 1 : 0;
+        }
+        sorted[below + same] = pos[q];
+        if (same == 0) first[v] = below;
+        atomicAdd(&count[v], 1);
+    }
+    __syncthreads();
+    const int groups = 256 / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    for (int v = group; v < nv; v += groups) {
+        const int c = count[v], f = c ? first[v] : 0;
+        if (c == 0 && a.accumulate) continue;
+        for (int d = lane * N; d < a.D; d += lanes * N) {
+            float s[N] = {};
+#pragma unroll 4
+            for (int q = 0; q < c; ++q) add_row<T, N>(a, sorted[f + q], d, s);
+            put_word<T, N>(a, v0 + v, d, s);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the sort
+
+// A stable radix sort of positions by word, kSortBits at most a pass; tokens
+// outside the table sort as word V, behind all others.  A pass: digits counted
+// per workgroup of kSortChunk positions; each digit's counts summed over the
+// workgroups; positions moved, ranked within a wave by matching lanes and
+// between waves by the waves' counts.
+constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
+constexpr int kSortRounds = kSortChunk / kSortThreads;
+constexpr int kMaxDigits = 1 << kSortBits;
+
+__device__ __forceinline__ int word_of(const EmbedBackwardArgs& a, int t) { return in_table(t, a.V) ? t : a.V; }
+
+// Workgroups behind the first `nb` fill the gradient with zeros.
+template <typename T>
+__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedBackwardArgs a, const int32_t* keys, int nb, int shift,
+                                                                   int digits, bool wide, int64_t fill_rows) {
+    __shared__ int hist[kMaxDigits];
+    if ((int)blockIdx.x >= nb) {
+        const int64_t r0 = (int64_t)(blockIdx.x - nb) * fill_rows, r1 = min((int64_t)a.V, r0 + fill_rows);
+        if (a.wstride == a.D && wide) {  // one run
+            u32x4* o = (u32x4*)((T*)a.gweight + r0 * a.D);
+            const int64_t n = (r1 - r0) * a.D * (int64_t)sizeof(T) / 16;
+            for (int64_t i = threadIdx.x; i < n; i += kSortThreads) o[i] = u32x4{0, 0, 0, 0};
+        } else {
+            for (int64_t r = r0; r < r1; ++r)
+                for (int d = threadIdx.x; d < a.D; d += kSortThreads) ((T*)a.gweight)[r * a.wstride + d] = 0;
+        }
+        return;
+    }
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) hist[d] = 0;
+    __syncthreads();
+    const int base = blockIdx.x * kSortChunk;
+#pragma unroll 4
+    for (int r = 0; r < kSortRounds; ++r) {
+        const int i = base + r * kSortThreads + threadIdx.x;
+        if (i < a.n) atomicAdd(&hist[((keys ? keys[i] : word_of(a, a.tokens[i])) >> shift) & (digits - 1)], 1);
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) a.ws.table[(int64_t)d * nb + blockIdx.x] = hist[d];
+}
+
+// A wave per digit: its workgroups' counts become the counts before them.
+__global__ __launch_bounds__(256) void embed_scan_kernel(EmbedBackwardArgs a, int nb, int digits) {
+    const int d = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (d >= digits) return;
+    int32_t* row = a.ws.table + (int64_t)d * nb;
+    int before = 0;
+    for (int b = 0; b < nb; b += 64) {
+        const int x = b + lane < nb ? row[b + lane] : 0;
+        const int inc = (int)wave_inclusive_scan((uint32_t)x);
+        if (b + lane < nb) row[b + lane] = before + inc - x;
+        before += read_lane(inc, 63);
+    }
+    if (lane == 0) a.ws.totals[d] = before;
+}
+
+__global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardArgs a, const int32_t* keys, const int32_t* from,
+                                                                  int32_t* keys_out, int32_t* to, int nb, int shift,
+                                                                  int bits) {
+    __shared__ int at[kSortWaves][kMaxDigits];
+    __shared__ int wsum[kSortWaves];
+    const int digits = 1 << bits, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int d = threadIdx.x; d < digits; d += kSortThreads)
+        for (int w = 0; w < kSortWaves; ++w) at[w][d] = 0;
+    __syncthreads();
+    // a wave's positions are consecutive: kSortRounds of 64
+    const int base = blockIdx.x * kSortChunk + wave * (kSortChunk / kSortWaves);
+    int key[kSortRounds];
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        const int i = base + r * 64 + lane;
+        key[r] = i < a.n ? (keys ? keys[i] : word_of(a, a.tokens[i])) : -1;
+        if (i < a.n) atomicAdd(&at[wave][(key[r] >> shift) & (digits - 1)], 1);
+    }
+    __syncthreads();
+    // where each wave's first position of each digit goes
+    int carry = 0;
+    for (int d0 = 0; d0 < digits; d0 += kSortThreads) {
+        const int d = d0 + threadIdx.x;
+        const int total = d < digits ? a.ws.totals[d] : 0;
+        const int inc = (int)wave_inclusive_scan((uint32_t)total);
+        if (lane == 63) wsum[wave] = inc;
+        __syncthreads();
+        int before = carry + inc - total;
+        for (int w = 0; w < wave; ++w) before += wsum[w];
+        for (int w = 0; w < kSortWaves; ++w) carry += wsum[w];
+        if (d < digits) {
+            int o = before + a.ws.table[(int64_t)d * nb + blockIdx.x];
+            for (int w = 0; w < kSortWaves; ++w) {
+                const int c = at[w][d];
+                at[w][d] = o;
+                o += c;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        const int i = base + r * 64 + lane;
+        const bool ok = i < a.n;
+        const int d = (key[r] >> shift) & (digits - 1);
+        uint64_t same = __ballot(ok);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t one = __ballot((d >> b) & 1);
+            same &= (d >> b) & 1 ? one : ~one;
+        }
+        const int rank = lanes_below(same);
+        int o = 0;
+        if (ok) o = at[wave][d];
+        __builtin_amdgcn_wave_barrier();  // every lane has read before the first of a digit moves its place on
+        if (ok && rank == 0) at[wave][d] = o + __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        if (ok) {
+            keys_out[o + rank] = key[r];
+            to[o + rank] = from ? from[i] : i;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the sums
+
+// Group g sums the sorted positions [g*tile, (g+1)*tile), word after word.
+// Sums of a word that lies in the tile are written; the tile's part of one that
+// began before it goes to part 0 of the tile, of one that goes on behind it to
+// part 1 (to part 0 if it did both).
+template <typename T, int N>
+__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, const int32_t* keys, const int32_t* pos, int lanes,
+                                                        int tile, int tiles) {
+    const int g = blockIdx.x * (256 / lanes) + threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    if (g >= tiles) return;
+    const int i0 = g * tile, i1 = min(a.n, i0 + tile);
+    const int before = i0 > 0 ? keys[i0 - 1] : -1, behind = i1 < a.n ? keys[i1] : a.V;
+    constexpr int kAhead = 8;
+    for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
+        float s[N] = {};
+        int v = keys[i0];
+        for (int i = i0; i < i1 && v < a.V; i += kAhead) {
+            float x[kAhead][N];
+            int k[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                k[u] = i + u < i1 ? keys[i + u] : a.V;
+                if (k[u] < a.V) Pack<T, N>::load((const T*)a.grad + (int64_t)pos[i + u] * a.gstride + d, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (k[u] != v && v < a.V) {  // v ends here
+                    if (v == before) {
+                        float* p = a.ws.parts + (int64_t)g * 2 * a.Dp + d;
+#pragma unroll
+                        for (int e = 0; e < N; ++e) p[e] = s[e];
+                    } else if (i + u < i1 || v != behind) {
+                        put_word<T, N>(a, v, d, s);
+                    } else {
+                        float* p = a.ws.parts + ((int64_t)g * 2 + 1) * a.Dp + d;
+#pragma unroll
+                        for (int e = 0; e < N; ++e) p[e] = s[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < N; ++e) s[e] = 0.0f;
+                }
+                if (k[u] < a.V) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) s[e] += x[u][e];
+                }
+                v = k[u];
+            }
+        }
+        // the tile's last position was the group's last of a round of kAhead
+        if (v < a.V) {
+            float* p = a.ws.parts + ((int64_t)g * 2 + (v == before ? 0 : 1)) * a.Dp + d;
+            const bool whole = v != before && v != behind;
+            if (whole) put_word<T, N>(a, v, d, s);
+            else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) p[e] = s[e];
+            }
+        }
+    }
+}
+
+// The words that cross tiles: group g takes the one that begins in tile g and
+// goes on behind it, and adds the tiles' parts in order.
+template <typename T, int N>
+__global__ __launch_bounds__(256) void embed_join_kernel(EmbedBackwardArgs a, const int32_t* keys, int lanes, int tile, int tiles) {
+    const int g = blockIdx.x * (256 / lanes) + threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    if (g >= tiles) return;
+    const int i0 = g * tile, i1 = i0 + tile;
+    if (i1 >= a.n) return;
+    const int v = keys[i1 - 1];
+    if (v >= a.V || keys[i1] != v || (i0 > 0 && keys[i0 - 1] == v)) return;
+    int last = g + 1, over = tiles;  // v reaches tile `last`, not tile `over`
+    while (over - last > 1) {
+        const int mid = (last + over) / 2;
+        if (keys[mid * tile] == v) last = mid;
+        else over = mid;
+    }
+    for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
+        float s[N];
+        const float* p = a.ws.parts + ((int64_t)g * 2 + 1) * a.Dp + d;
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] = p[e];
+#pragma unroll 8
+        for (int q = g + 1; q <= last; ++q) {
+            const float* x = a.ws.parts + (int64_t)q * 2 * a.Dp + d;
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e] += x[e];
+        }
+        put_word<T, N>(a, v, d, s);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <typename T>
+bool rows_wide(const void* p, int64_t stride, int D) {
+    const int n = 16 / (int)sizeof(T);
+    return (uintptr_t)p % 16 == 0 && stride % n == 0 && D % n == 0;
+}
+
+// Threads to a row of `chunks` loads: a power of two, at most 256.
+int lanes_for(int chunks) {
+    int l = 1;
+    while (l < chunks && l < 256) l *= 2;
+    return l;
+}
+
+template <typename T, int N>
+hipError_t lookup_t(const EmbedLookupArgs& a, hipStream_t st) {
+    const int lanes = lanes_for((a.D + N - 1) / N), groups = 256 / lanes;
+    // four rows a group once that still leaves several workgroups to a CU
+    const int per = a.n >= 4 * 2048 * groups ? 4 : 1;
+    const dim3 grid((unsigned)((a.n + (int64_t)groups * per - 1) / (groups * per)));
+    if (per == 4) embed_lookup_kernel<T, N, 4><<<grid, 256, 0, st>>>(a, lanes);
+    else embed_lookup_kernel<T, N, 1><<<grid, 256, 0, st>>>(a, lanes);
+    return hipGetLastError();
+}
+
+template <typename T, int N>
+hipError_t backward_t(const EmbedBackwardArgs& a, hipStream_t st) {
+    const int chunks = (a.D + N - 1) / N;
+    const int lanes = lanes_for(chunks), groups = 256 / lanes;
+    if (a.n <= kEmbedFew) {
+        // about 32 KB of the gradient to a workgroup
+        int words = (int)((32 << 10) / ((int64_t)a.D * sizeof(T)));
+        words = words < groups ? groups : (words < kFewWords ? words : kFewWords);
+        embed_few_kernel<T, N><<<dim3((unsigned)((a.V + words - 1) / words)), 256, 0, st>>>(a, lanes, words);
+        return hipGetLastError();
+    }
+    const EmbedPlan p = embed_plan(a.n, a.V, a.D);
+    const int64_t fill_rows = a.accumulate ? 0 : ((128 << 10) + (int64_t)a.D * sizeof(T) - 1) / ((int64_t)a.D * sizeof(T));
+    const int fill = a.accumulate ? 0 : (int)((a.V + fill_rows - 1) / fill_rows);
+    const int32_t *keys = nullptr, *pos = nullptr;
+    for (int q = 0; q < p.passes; ++q) {
+        const int shift = q * p.bits, out = q & 1;
+        embed_count_kernel<T><<<dim3((unsigned)(p.blocks + (q == 0 ? fill : 0))), kSortThreads, 0, st>>>(
+            a, keys, p.blocks, shift, 1 << p.bits, N > 1, fill_rows);
+        embed_scan_kernel<<<dim3((unsigned)(((1 << p.bits) + 3) / 4)), 256, 0, st>>>(a, p.blocks, 1 << p.bits);
+        embed_move_kernel<<<dim3((unsigned)p.blocks), kSortThreads, 0, st>>>(a, keys, pos, a.ws.keys[out], a.ws.pos[out], p.blocks,
+                                                                            shift, p.bits);
+        keys = a.ws.keys[out];
+        pos = a.ws.pos[out];
+    }
+    const dim3 grid((unsigned)((p.tiles + groups - 1) / groups));
+    embed_sum_kernel<T, N><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
+    embed_join_kernel<T, N><<<grid, 256, 0, st>>>(a, keys, lanes, p.tile, p.tiles);
+    return hipGetLastError();
 }
 
 }  // namespace
 
+EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim) {
+    (void)dim;
+    EmbedPlan p{};
+    int bits = 1;
+    while ((vocab >> bits) > 0) ++bits;  // words 0 .. vocab
+    p.passes = (bits + kSortBits - 1) / kSortBits;
+    p.bits = (bits + p.passes - 1) / p.passes;
+    p.blocks = (int)((n + kSortChunk - 1) / kSortChunk);
+    p.tile = 64;
+    while ((n + p.tile - 1) / p.tile > 16384) p.tile *= 2;  // bounds the parts' memory
+    p.tiles = (int)((n + p.tile - 1) / p.tile);
+    return p;
+}
+
 hipError_t launch_embed_lookup(const EmbedLookupArgs& a, int dtype, hipStream_t st) {
     if (a.n == 0) return hipSuccess;
-    if (dtype == GR_BF16) embed_lookup_kernel<uint16_t><<<dim3((unsigned)a.n), 256, 0, st>>>(a);
-    else embed_lookup_kernel<float><<<dim3((unsigned)a.n), 256, 0, st>>>(a);
-    return hipGetLastError();
+    if (dtype == GR_BF16)
+        return rows_wide<uint16_t>(a.weight, a.wstride, a.D) && rows_wide<uint16_t>(a.out, a.ostride, a.D)
+                   ? lookup_t<uint16_t, 8>(a, st) : lookup_t<uint16_t, 1>(a, st);
+    return rows_wide<float>(a.weight, a.wstride, a.D) && rows_wide<float>(a.out, a.ostride, a.D) ? lookup_t<float, 4>(a, st)
+                                                                                               : lookup_t<float, 1>(a, st);
 }
 
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, int dtype, hipStream_t st) {
     if (a.n == 0 && a.accumulate) return hipSuccess;
-    if (dtype == GR_BF16) embed_backward_kernel<uint16_t><<<dim3((unsigned)a.V), 256, 0, st>>>(a);
-    else embed_backward_kernel<float><<<dim3((unsigned)a.V), 256, 0, st>>>(a);
-    return hipGetLastError();
+    if (dtype == GR_BF16)
+        return rows_wide<uint16_t>(a.grad, a.gstride, a.D) && rows_wide<uint16_t>(a.gweight, a.wstride, a.D)
+                   ? backward_t<uint16_t, 8>(a, st) : backward_t<uint16_t, 1>(a, st);
+    return rows_wide<float>(a.grad, a.gstride, a.D) && rows_wide<float>(a.gweight, a.wstride, a.D) ? backward_t<float, 4>(a, st)
+                                                                                                 : backward_t<float, 1>(a, st);
 }
 
 }  // namespace gr

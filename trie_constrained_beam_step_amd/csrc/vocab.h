@@ -17,15 +17,36 @@ struct EmbedLookupArgs {
     int64_t ostride;
 };
 
+constexpr int kEmbedFew = 512;    // at most so many tokens: no sort
+constexpr int kSortBits = 11;     // of a sort pass at most
+constexpr int kSortChunk = 4096;  // positions of a sort workgroup
+
+struct EmbedPlan {
+    int32_t passes, bits, blocks;  // of the sort
+    int32_t tile, tiles;           // of the sums
+};
+
+EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim);
+
+// The gradient's workspace (device).
+struct EmbedSpace {
+    int32_t* keys[2];  // [n] words in sorted order, by turns
+    int32_t* pos[2];   // [n] their positions
+    int32_t* table;    // [digits][workgroups] counts
+    int32_t* totals;   // [digits]
+    float* parts;      // [tiles][2][Dp] sums of words that cross tiles
+};
+
 struct EmbedBackwardArgs {
     const int32_t* tokens;  // [n]
-    int32_t n, V, D;
+    int32_t n, V, D, Dp;    // Dp: D rounded up to 8
     float scale;
     const void* grad;    // [n] rows of D elements, gstride apart
     int64_t gstride;
     void* gweight;       // [V] rows, wstride apart
     int64_t wstride;
     int32_t accumulate;
+    EmbedSpace ws;
 };
 
 // Sizes of a head's workspace, fixed at init for its most rows.

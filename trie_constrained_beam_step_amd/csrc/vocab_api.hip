@@ -72,6 +72,7 @@ gr_status init_fail(hipError_t e, const char* what) {
 struct gr_embed {
     gr_embed_config cfg{};
     int device = 0;
+    gr::EmbedSpace ws{};
 };
 
 struct gr_head {
@@ -88,6 +89,15 @@ struct gr_head {
 
 // ------------------------------------------------------------- embedding
 
+static int32_t embed_width(int32_t dim) { return (dim + 7) / 8 * 8; }
+
+static void embed_release(gr_embed* h) {
+    const gr::EmbedSpace& w = h->ws;
+    void* all[] = {w.keys[0], w.keys[1], w.pos[0], w.pos[1], w.table, w.totals, w.parts};
+    for (void* p : all) (void)hipFree(p);
+    delete h;
+}
+
 extern "C" gr_status gr_embed_init(const gr_embed_config* cfg, gr_stream stream, gr_embed** out) {
     if (!cfg || !out) return fail(GR_ERR_INVALID_ARG, "NULL config or out");
     GR_TRY(check_common(cfg->vocab, cfg->dim, cfg->dtype, cfg->scale));
@@ -100,6 +110,26 @@ extern "C" gr_status gr_embed_init(const gr_embed_config* cfg, gr_stream stream,
     h->cfg = *cfg;
     h->device = dev;
     (void)stream;
+    hipError_t e = hipSuccess;
+    if (cfg->max_tokens > gr::kEmbedFew) {
+        // a smaller call's sort has fewer workgroups, its sums fewer tiles or
+        // (16,384 of them at most) smaller ones: sizes for the most tokens and
+        // for the most tiles cover it
+        const size_t n = cfg->max_tokens;
+        const gr::EmbedPlan p = gr::embed_plan(n, cfg->vocab, cfg->dim);
+        const size_t tiles = n / 64 + 1 < 16384 ? n / 64 + 1 : 16384;
+        for (int i = 0; i < 2 && e == hipSuccess; ++i) {
+            e = dalloc(&h->ws.keys[i], n);
+            if (e == hipSuccess) e = dalloc(&h->ws.pos[i], n);
+        }
+        if (e == hipSuccess) e = dalloc(&h->ws.table, ((size_t)1 << p.bits) * p.blocks);
+        if (e == hipSuccess) e = dalloc(&h->ws.totals, (size_t)1 << p.bits);
+        if (e == hipSuccess) e = dalloc(&h->ws.parts, tiles * 2 * embed_width(cfg->dim));
+    }
+    if (e != hipSuccess) {
+        embed_release(h);
+        return init_fail(e, "embedding workspace");
+    }
     *out = h;
     return GR_OK;
 }
@@ -151,6 +181,8 @@ extern "C" gr_status gr_embed_backward(gr_embed* h, const int32_t* d_tokens, int
     a.gweight = d_grad_weight;
     a.wstride = grad_weight_row_stride;
     a.accumulate = accumulate != 0;
+    a.Dp = embed_width(c.dim);
+    a.ws = h->ws;
     OnDevice on(h->device);
     HIP_TRY(on.err, "set device");
     HIP_TRY(gr::launch_embed_backward(a, c.dtype, (hipStream_t)stream), "embedding backward launch");
@@ -159,11 +191,9 @@ extern "C" gr_status gr_embed_backward(gr_embed* h, const int32_t* d_tokens, int
 
 extern "C" void gr_embed_free(gr_embed* h) {
     if (!h) return;
-    {
-        OnDevice on(h->device);
-        (void)hipDeviceSynchronize();
-    }
-    delete h;
+    OnDevice on(h->device);
+    (void)hipDeviceSynchronize();
+    embed_release(h);
 }
 
 // ------------------------------------------------------------------ head
