@@ -391,17 +391,19 @@ class _Table:
             return stream
         return torch.cuda.ExternalStream(int(stream), device=self.device)
 
-    def _empty(self, shape, dtype, s):
+    def _empty(self, shape, dtype, stream):
         """A new output, owned by the stream that writes it."""
         import torch
-        with torch.cuda.stream(s):
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self._stream(stream)):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _used(self, s, *tensors):
-        """Tensors of the caller's current stream that work on `s` reads or
-        writes: their memory is not reused before that work is done."""
-        import torch
-        if s != torch.cuda.current_stream(self.device):
+    def _used(self, stream, *tensors):
+        """Tensors that work on a `stream` given by the caller reads or writes:
+        their memory is not reused before that work is done."""
+        if stream is not None:
+            s = self._stream(stream)
             for t in tensors:
                 if t is not None:
                     t.record_stream(s)
@@ -445,10 +447,10 @@ class Embedding(_Table):
         pw, sw = self._rows(weight, "weight", self.vocab)
         s = self._stream(stream)
         if out is None:
-            out = self._empty((*tokens.shape, self.dim), self._torch_dtype, s)
+            out = self._empty((*tokens.shape, self.dim), self._torch_dtype, stream)
         po, so = self._rows(out, "out", n)
         _check(lib().gr_embed_lookup(self.handle, pt, n, pw, sw, po, so, s.cuda_stream))
-        self._used(s, tokens, weight)
+        self._used(stream, tokens, weight)
         return out
 
     def backward(self, tokens, grad, grad_weight=None, accumulate: bool = False, stream=None):
@@ -463,10 +465,10 @@ class Embedding(_Table):
         if grad_weight is None:
             if accumulate:
                 raise ValueError("accumulate needs the grad_weight to add to")
-            grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, s)
+            grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, stream)
         pw, sw = self._rows(grad_weight, "grad_weight", self.vocab)
         _check(lib().gr_embed_backward(self.handle, pt, n, pg, sg, pw, sw, 1 if accumulate else 0, s.cuda_stream))
-        self._used(s, tokens, grad, grad_weight)
+        self._used(stream, tokens, grad, grad_weight)
         return grad_weight
 
 
@@ -499,9 +501,9 @@ class Head(_Table):
         ph, sh = self._rows(hidden, "hidden", n)
         pw, sw = self._rows(weight, "weight", self.vocab)
         s = self._stream(stream)
-        loss, lse = (self._empty(targets.shape, torch.float32, s) for _ in range(2))
+        loss, lse = (self._empty(targets.shape, torch.float32, stream) for _ in range(2))
         _check(lib().gr_head_loss(self.handle, ph, sh, pw, sw, pt, n, loss.data_ptr(), lse.data_ptr(), s.cuda_stream))
-        self._used(s, hidden, weight, targets)
+        self._used(stream, hidden, weight, targets)
         return loss, lse
 
     def backward(self, hidden, weight, targets, lse, grad_loss, grad_hidden=None, grad_weight=None,
@@ -527,7 +529,7 @@ class Head(_Table):
             grad_hidden = None
         else:
             if grad_hidden is None:
-                grad_hidden = self._empty(hidden.shape, self._torch_dtype, s)
+                grad_hidden = self._empty(hidden.shape, self._torch_dtype, stream)
             pgh, sgh = self._rows(grad_hidden, "grad_hidden", n)
         if "weight" not in need:
             grad_weight = None
@@ -535,11 +537,11 @@ class Head(_Table):
             if grad_weight is None:
                 if accumulate:
                     raise ValueError("accumulate needs the grad_weight to add to")
-                grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, s)
+                grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, stream)
             pgw, sgw = self._rows(grad_weight, "grad_weight", self.vocab)
         _check(lib().gr_head_backward(self.handle, ph, sh, pw, sw, pt, n, pl, pg, pgh, sgh, pgw, sgw,
                                       1 if accumulate else 0, s.cuda_stream))
-        self._used(s, hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
+        self._used(stream, hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
         return grad_hidden, grad_weight
 
 

@@ -183,23 +183,36 @@ constexpr int kMaxDigits = 1 << kSortBits;
 
 __device__ __forceinline__ int word_of(const EmbedBackwardArgs& a, int t) { return in_table(t, a.V) ? t : a.V; }
 
-// Workgroups behind the first `nb` fill the gradient with zeros.
-template <typename T>
-__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedBackwardArgs a, const int32_t* keys, int nb, int shift,
-                                                                   int digits, bool wide, int64_t fill_rows) {
-    __shared__ int hist[kMaxDigits];
-    if ((int)blockIdx.x >= nb) {
-        const int64_t r0 = (int64_t)(blockIdx.x - nb) * fill_rows, r1 = min((int64_t)a.V, r0 + fill_rows);
-        if (a.wstride == a.D && wide) {  // one run
-            u32x4* o = (u32x4*)((T*)a.gweight + r0 * a.D);
-            const int64_t n = (r1 - r0) * a.D * (int64_t)sizeof(T) / 16;
-            for (int64_t i = threadIdx.x; i < n; i += kSortThreads) o[i] = u32x4{0, 0, 0, 0};
-        } else {
-            for (int64_t r = r0; r < r1; ++r)
-                for (int d = threadIdx.x; d < a.D; d += kSortThreads) ((T*)a.gweight)[r * a.wstride + d] = 0;
-        }
+// The zeros under the gradient's rows are written beside the sort, whose own
+// work leaves most of the chip idle: each of its launches carries a share of
+// the fill as further workgroups.  On 16,384 tokens of 151,936 words (311 MB of
+// zeros) that hides the sort behind the fill.
+struct Fill {
+    int first;      // fill workgroup of this launch's first
+    int64_t rows;   // of a fill workgroup
+    int32_t size;   // bytes of an element
+    int32_t wide;   // rows of whole 16-byte chunks
+};
+
+__device__ void fill_zeros(const EmbedBackwardArgs& a, const Fill& f, int wg) {
+    const int64_t r0 = (int64_t)(f.first + wg) * f.rows, r1 = min((int64_t)a.V, r0 + f.rows);
+    if (f.wide && a.wstride == a.D) {  // one run
+        u32x4* o = (u32x4*)((char*)a.gweight + r0 * a.D * f.size);
+        const int64_t n = (r1 - r0) * a.D * f.size / 16;
+        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = u32x4{0, 0, 0, 0};
         return;
     }
+    for (int64_t r = r0; r < r1; ++r)
+        for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
+            if (f.size == 2) ((uint16_t*)a.gweight)[r * a.wstride + d] = 0;
+            else ((uint32_t*)a.gweight)[r * a.wstride + d] = 0;
+        }
+}
+
+__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedBackwardArgs a, const int32_t* keys, int nb, int shift,
+                                                                   int digits, Fill fill) {
+    __shared__ int hist[kMaxDigits];
+    if ((int)blockIdx.x >= nb) return fill_zeros(a, fill, blockIdx.x - nb);
     for (int d = threadIdx.x; d < digits; d += kSortThreads) hist[d] = 0;
     __syncthreads();
     const int base = blockIdx.x * kSortChunk;
@@ -213,7 +226,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedBackward
 }
 
 // A wave per digit: its workgroups' counts become the counts before them.
-__global__ __launch_bounds__(256) void embed_scan_kernel(EmbedBackwardArgs a, int nb, int digits) {
+__global__ __launch_bounds__(256) void embed_scan_kernel(EmbedBackwardArgs a, int nb, int digits, int own, Fill fill) {
+    if ((int)blockIdx.x >= own) return fill_zeros(a, fill, blockIdx.x - own);
     const int d = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (d >= digits) return;
     int32_t* row = a.ws.table + (int64_t)d * nb;
@@ -229,9 +243,10 @@ __global__ __launch_bounds__(256) void embed_scan_kernel(EmbedBackwardArgs a, in
 
 __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardArgs a, const int32_t* keys, const int32_t* from,
                                                                   int32_t* keys_out, int32_t* to, int nb, int shift,
-                                                                  int bits) {
+                                                                  int bits, Fill fill) {
     __shared__ int at[kSortWaves][kMaxDigits];
     __shared__ int wsum[kSortWaves];
+    if ((int)blockIdx.x >= nb) return fill_zeros(a, fill, blockIdx.x - nb);
     const int digits = 1 << bits, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (int d = threadIdx.x; d < digits; d += kSortThreads)
         for (int w = 0; w < kSortWaves; ++w) at[w][d] = 0;
@@ -307,13 +322,25 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
     for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
         float s[N] = {};
         int v = keys[i0];
+        int kn[kAhead], pn[kAhead];  // the next round's words and positions
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            kn[u] = i0 + u < i1 ? keys[i0 + u] : a.V;
+            pn[u] = i0 + u < i1 ? pos[i0 + u] : 0;
+        }
         for (int i = i0; i < i1 && v < a.V; i += kAhead) {
             float x[kAhead][N];
             int k[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                k[u] = i + u < i1 ? keys[i + u] : a.V;
-                if (k[u] < a.V) Pack<T, N>::load((const T*)a.grad + (int64_t)pos[i + u] * a.gstride + d, x[u]);
+                k[u] = kn[u];
+                if (k[u] < a.V) Pack<T, N>::load((const T*)a.grad + (int64_t)pn[u] * a.gstride + d, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int q = i + kAhead + u;
+                kn[u] = q < i1 ? keys[q] : a.V;
+                pn[u] = q < i1 ? pos[q] : 0;
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -352,34 +379,55 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
     }
 }
 
-// The words that cross tiles: group g takes the one that begins in tile g and
-// goes on behind it, and adds the tiles' parts in order.
+// The words that cross tiles: workgroup g takes the one that begins in tile g
+// and goes on behind it.  Its groups of threads each add a run of the tiles'
+// parts in order, and the runs' sums are added in order.
+constexpr int kJoinThreads = 512;
+
 template <typename T, int N>
-__global__ __launch_bounds__(256) void embed_join_kernel(EmbedBackwardArgs a, const int32_t* keys, int lanes, int tile, int tiles) {
-    const int g = blockIdx.x * (256 / lanes) + threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    if (g >= tiles) return;
+__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedBackwardArgs a, const int32_t* keys, int lanes, int tile,
+                                                                  int tiles) {
+    __shared__ float runs[kJoinThreads * N];
+    const int g = blockIdx.x;
     const int i0 = g * tile, i1 = i0 + tile;
     if (i1 >= a.n) return;
     const int v = keys[i1 - 1];
     if (v >= a.V || keys[i1] != v || (i0 > 0 && keys[i0 - 1] == v)) return;
-    int last = g + 1, over = tiles;  // v reaches tile `last`, not tile `over`
+    // v reaches tile `last`, not tile `over`: most words end soon
+    int last = g + 1, over = g + 2;
+    while (over < tiles && keys[over * tile] == v) {
+        last = over;
+        over = min(tiles, g + 2 * (over - g));
+    }
     while (over - last > 1) {
         const int mid = (last + over) / 2;
         if (keys[mid * tile] == v) last = mid;
         else over = mid;
     }
-    for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
-        float s[N];
-        const float* p = a.ws.parts + ((int64_t)g * 2 + 1) * a.Dp + d;
-#pragma unroll
-        for (int e = 0; e < N; ++e) s[e] = p[e];
+    const int groups = kJoinThreads / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int per = (last - g + groups) / groups;  // of the parts g .. last
+    const int q0 = g + group * per, q1 = min(last + 1, q0 + per);
+    for (int d0 = 0; d0 < a.D; d0 += lanes * N) {
+        const int d = d0 + lane * N;
+        float s[N] = {};
+        if (d < a.D) {
 #pragma unroll 8
-        for (int q = g + 1; q <= last; ++q) {
-            const float* x = a.ws.parts + (int64_t)q * 2 * a.Dp + d;
+            for (int q = q0; q < q1; ++q) {
+                const float* x = a.ws.parts + ((int64_t)q * 2 + (q == g ? 1 : 0)) * a.Dp + d;
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[e] += x[e];
+                for (int e = 0; e < N; ++e) s[e] += x[e];
+            }
         }
-        put_word<T, N>(a, v, d, s);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < N; ++e) runs[e * kJoinThreads + threadIdx.x] = s[e];
+        __syncthreads();
+        if (group == 0 && d < a.D) {
+            for (int r = 1; r < groups; ++r)
+#pragma unroll
+                for (int e = 0; e < N; ++e) s[e] += runs[e * kJoinThreads + r * lanes + lane];
+            put_word<T, N>(a, v, d, s);
+        }
     }
 }
 
@@ -420,38 +468,49 @@ hipError_t backward_t(const EmbedBackwardArgs& a, hipStream_t st) {
         embed_few_kernel<T, N><<<dim3((unsigned)((a.V + words - 1) / words)), 256, 0, st>>>(a, lanes, words);
         return hipGetLastError();
     }
-    const EmbedPlan p = embed_plan(a.n, a.V, a.D);
-    const int64_t fill_rows = a.accumulate ? 0 : ((128 << 10) + (int64_t)a.D * sizeof(T) - 1) / ((int64_t)a.D * sizeof(T));
-    const int fill = a.accumulate ? 0 : (int)((a.V + fill_rows - 1) / fill_rows);
+    const EmbedPlan p = embed_plan(a.n, a.V, lanes);
+    // fill workgroups of about 128 KB, spread over the sort's launches
+    const int64_t row_bytes = (int64_t)a.D * sizeof(T);
+    Fill f{0, ((128 << 10) + row_bytes - 1) / row_bytes, (int32_t)sizeof(T), N > 1};
+    const int fills = a.accumulate ? 0 : (int)((a.V + f.rows - 1) / f.rows);
+    int launch = 0;
+    const auto share = [&]() {  // sets f.first, returns the launch's fill workgroups
+        f.first = (int)((int64_t)fills * launch / (3 * p.passes));
+        ++launch;
+        return (int)((int64_t)fills * launch / (3 * p.passes)) - f.first;
+    };
     const int32_t *keys = nullptr, *pos = nullptr;
     for (int q = 0; q < p.passes; ++q) {
-        const int shift = q * p.bits, out = q & 1;
-        embed_count_kernel<T><<<dim3((unsigned)(p.blocks + (q == 0 ? fill : 0))), kSortThreads, 0, st>>>(
-            a, keys, p.blocks, shift, 1 << p.bits, N > 1, fill_rows);
-        embed_scan_kernel<<<dim3((unsigned)(((1 << p.bits) + 3) / 4)), 256, 0, st>>>(a, p.blocks, 1 << p.bits);
-        embed_move_kernel<<<dim3((unsigned)p.blocks), kSortThreads, 0, st>>>(a, keys, pos, a.ws.keys[out], a.ws.pos[out], p.blocks,
-                                                                            shift, p.bits);
+        const int shift = q * p.bits, out = q & 1, digits = 1 << p.bits, scans = (digits + 3) / 4;
+        int more = share();
+        embed_count_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, 0, st>>>(a, keys, p.blocks, shift, digits, f);
+        more = share();
+        embed_scan_kernel<<<dim3((unsigned)(scans + more)), 256, 0, st>>>(a, p.blocks, digits, scans, f);
+        more = share();
+        embed_move_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, 0, st>>>(a, keys, pos, a.ws.keys[out], a.ws.pos[out],
+                                                                                     p.blocks, shift, p.bits, f);
         keys = a.ws.keys[out];
         pos = a.ws.pos[out];
     }
     const dim3 grid((unsigned)((p.tiles + groups - 1) / groups));
     embed_sum_kernel<T, N><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
-    embed_join_kernel<T, N><<<grid, 256, 0, st>>>(a, keys, lanes, p.tile, p.tiles);
+    embed_join_kernel<T, N><<<dim3((unsigned)p.tiles), kJoinThreads, 0, st>>>(a, keys, lanes, p.tile, p.tiles);
     return hipGetLastError();
 }
 
 }  // namespace
 
-EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim) {
-    (void)dim;
+EmbedPlan embed_plan(int64_t n, int64_t vocab, int lanes) {
     EmbedPlan p{};
     int bits = 1;
     while ((vocab >> bits) > 0) ++bits;  // words 0 .. vocab
     p.passes = (bits + kSortBits - 1) / kSortBits;
     p.bits = (bits + p.passes - 1) / p.passes;
     p.blocks = (int)((n + kSortChunk - 1) / kSortChunk);
-    p.tile = 64;
-    while ((n + p.tile - 1) / p.tile > 16384) p.tile *= 2;  // bounds the parts' memory
+    // small tiles spread the rows over the chip (2^18 threads fill it), large
+    // ones leave fewer parts to join and bound their memory
+    p.tile = 8;
+    while (n * lanes / (2 * p.tile) >= (1 << 18) || (n + p.tile - 1) / p.tile > kSumTiles) p.tile *= 2;
     p.tiles = (int)((n + p.tile - 1) / p.tile);
     return p;
 }

@@ -19,14 +19,16 @@ struct EmbedLookupArgs {
 
 constexpr int kEmbedFew = 512;    // at most so many tokens: no sort
 constexpr int kSortBits = 11;     // of a sort pass at most
-constexpr int kSortChunk = 4096;  // positions of a sort workgroup
+constexpr int kSortChunk = 1024;  // positions of a sort workgroup
+constexpr int kSumTiles = 8192;   // tiles of the sums at most
 
 struct EmbedPlan {
     int32_t passes, bits, blocks;  // of the sort
     int32_t tile, tiles;           // of the sums
 };
 
-EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim);
+// lanes: threads to a row in the sums
+EmbedPlan embed_plan(int64_t n, int64_t vocab, int lanes);
 
 // The gradient's workspace (device).
 struct EmbedSpace {

@@ -112,12 +112,11 @@ extern "C" gr_status gr_embed_init(const gr_embed_config* cfg, gr_stream stream,
     (void)stream;
     hipError_t e = hipSuccess;
     if (cfg->max_tokens > gr::kEmbedFew) {
-        // a smaller call's sort has fewer workgroups, its sums fewer tiles or
-        // (16,384 of them at most) smaller ones: sizes for the most tokens and
-        // for the most tiles cover it
+        // a smaller call's sort has fewer workgroups; its sums may have more
+        // (smaller) tiles than the largest call's, but no more than the limits here
         const size_t n = cfg->max_tokens;
-        const gr::EmbedPlan p = gr::embed_plan(n, cfg->vocab, cfg->dim);
-        const size_t tiles = n / 64 + 1 < 16384 ? n / 64 + 1 : 16384;
+        const gr::EmbedPlan p = gr::embed_plan(n, cfg->vocab, 256);
+        const size_t tiles = n / 8 + 1 < gr::kSumTiles ? n / 8 + 1 : gr::kSumTiles;
         for (int i = 0; i < 2 && e == hipSuccess; ++i) {
             e = dalloc(&h->ws.keys[i], n);
             if (e == hipSuccess) e = dalloc(&h->ws.pos[i], n);
