@@ -23,33 +23,31 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// N consecutive elements as fp32: 16 bytes of them, or one.
+// N consecutive elements: 16 bytes of them, or one.  Raw is how they are loaded,
+// value(raw, e) element e as fp32.
 template <typename T, int N>
 struct Pack;
 template <typename T>
 struct Pack<T, 1> {
-    static __device__ __forceinline__ void load(const T* p, float (&x)[1]) { x[0] = load_elem(p, 0); }
+    typedef T Raw;
+    static __device__ __forceinline__ Raw raw(const T* p) { return *p; }
+    static __device__ __forceinline__ float value(const Raw& r, int) { return load_elem(&r, 0); }
     static __device__ __forceinline__ void store(float* p, const float (&x)[1]) { *p = x[0]; }
     static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[1]) { *p = bf16_bits(x[0]); }
 };
 template <>
 struct Pack<float, 4> {
-    static __device__ __forceinline__ void load(const float* p, float (&x)[4]) {
-        const f32x4v v = *(const f32x4v*)p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = v[e];
-    }
+    typedef f32x4v Raw;
+    static __device__ __forceinline__ Raw raw(const float* p) { return *(const f32x4v*)p; }
+    static __device__ __forceinline__ float value(const Raw& r, int e) { return r[e]; }
     static __device__ __forceinline__ void store(float* p, const float (&x)[4]) { *(f32x4v*)p = f32x4v{x[0], x[1], x[2], x[3]}; }
 };
 template <>
 struct Pack<uint16_t, 8> {
-    static __device__ __forceinline__ void load(const uint16_t* p, float (&x)[8]) {
-        const u32x4 v = *(const u32x4*)p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(v[e] << 16);
-            x[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
-        }
+    typedef u32x4 Raw;
+    static __device__ __forceinline__ Raw raw(const uint16_t* p) { return *(const u32x4*)p; }
+    static __device__ __forceinline__ float value(const Raw& r, int e) {
+        return __uint_as_float(e & 1 ? r[e >> 1] & 0xFFFF0000u : r[e >> 1] << 16);
     }
     static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[8]) {
         u32x4 v;
@@ -64,10 +62,9 @@ template <typename T, int N>
 __device__ __forceinline__ void put_word(const EmbedBackwardArgs& a, int v, int d, float (&s)[N]) {
     T* o = (T*)a.gweight + (int64_t)v * a.wstride + d;
     if (a.accumulate) {
-        float old[N];
-        Pack<T, N>::load(o, old);
+        const typename Pack<T, N>::Raw old = Pack<T, N>::raw(o);
 #pragma unroll
-        for (int e = 0; e < N; ++e) s[e] = fmaf(s[e], a.scale, old[e]);
+        for (int e = 0; e < N; ++e) s[e] = fmaf(s[e], a.scale, Pack<T, N>::value(old, e));
     } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) s[e] *= a.scale;
@@ -77,10 +74,9 @@ __device__ __forceinline__ void put_word(const EmbedBackwardArgs& a, int v, int 
 
 template <typename T, int N>
 __device__ __forceinline__ void add_row(const EmbedBackwardArgs& a, int i, int d, float (&s)[N]) {
-    float x[N];
-    Pack<T, N>::load((const T*)a.grad + (int64_t)i * a.gstride + d, x);
+    const typename Pack<T, N>::Raw x = Pack<T, N>::raw((const T*)a.grad + (int64_t)i * a.gstride + d);
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[e] += x[e];
+    for (int e = 0; e < N; ++e) s[e] += Pack<T, N>::value(x, e);
 }
 
 constexpr int kFewWords = 512;  // words of an embed_few_kernel workgroup at most
@@ -99,19 +95,17 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(EmbedLookupArgs a, in
 #pragma unroll
     for (int r = 0; r < R; ++r) t[r] = i0 + r < a.n ? a.tokens[i0 + r] : -1;
     for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
-        float x[R][N];
+        typename Pack<T, N>::Raw x[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[r][e] = 0.0f;
-            if (in_table(t[r], a.V)) Pack<T, N>::load((const T*)a.weight + (int64_t)t[r] * a.wstride + d, x[r]);
-        }
+        for (int r = 0; r < R; ++r)
+            if (in_table(t[r], a.V)) x[r] = Pack<T, N>::raw((const T*)a.weight + (int64_t)t[r] * a.wstride + d);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (i0 + r >= a.n) break;
+            float y[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[r][e] = in_table(t[r], a.V) ? x[r][e] * a.scale : 0.0f;
-            Pack<T, N>::store((T*)a.out + (i0 + r) * a.ostride + d, x[r]);
+            for (int e = 0; e < N; ++e) y[e] = in_table(t[r], a.V) ? Pack<T, N>::value(x[r], e) * a.scale : 0.0f;
+            Pack<T, N>::store((T*)a.out + (i0 + r) * a.ostride + d, y);
         }
     }
 }
@@ -179,7 +173,6 @@ __global__ __launch_bounds__(256) void embed_few_kernel(EmbedBackwardArgs a, int
 // between waves by the waves' counts.
 constexpr int kSortThreads = 256, kSortWaves = kSortThreads / 64;
 constexpr int kSortRounds = kSortChunk / kSortThreads;
-constexpr int kMaxDigits = 1 << kSortBits;
 
 __device__ __forceinline__ int word_of(const EmbedBackwardArgs& a, int t) { return in_table(t, a.V) ? t : a.V; }
 
@@ -211,7 +204,7 @@ __device__ void fill_zeros(const EmbedBackwardArgs& a, const Fill& f, int wg) {
 
 __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedBackwardArgs a, const int32_t* keys, int nb, int shift,
                                                                    int digits, Fill fill) {
-    __shared__ int hist[kMaxDigits];
+    extern __shared__ int hist[];  // [digits]
     if ((int)blockIdx.x >= nb) return fill_zeros(a, fill, blockIdx.x - nb);
     for (int d = threadIdx.x; d < digits; d += kSortThreads) hist[d] = 0;
     __syncthreads();
@@ -244,12 +237,12 @@ __global__ __launch_bounds__(256) void embed_scan_kernel(EmbedBackwardArgs a, in
 __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardArgs a, const int32_t* keys, const int32_t* from,
                                                                   int32_t* keys_out, int32_t* to, int nb, int shift,
                                                                   int bits, Fill fill) {
-    __shared__ int at[kSortWaves][kMaxDigits];
+    extern __shared__ int at[];  // [waves][digits]
     __shared__ int wsum[kSortWaves];
     if ((int)blockIdx.x >= nb) return fill_zeros(a, fill, blockIdx.x - nb);
     const int digits = 1 << bits, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (int d = threadIdx.x; d < digits; d += kSortThreads)
-        for (int w = 0; w < kSortWaves; ++w) at[w][d] = 0;
+        for (int w = 0; w < kSortWaves; ++w) at[(w << bits) + d] = 0;
     __syncthreads();
     // a wave's positions are consecutive: kSortRounds of 64
     const int base = blockIdx.x * kSortChunk + wave * (kSortChunk / kSortWaves);
@@ -258,7 +251,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardA
     for (int r = 0; r < kSortRounds; ++r) {
         const int i = base + r * 64 + lane;
         key[r] = i < a.n ? (keys ? keys[i] : word_of(a, a.tokens[i])) : -1;
-        if (i < a.n) atomicAdd(&at[wave][(key[r] >> shift) & (digits - 1)], 1);
+        if (i < a.n) atomicAdd(&at[(wave << bits) + ((key[r] >> shift) & (digits - 1))], 1);
     }
     __syncthreads();
     // where each wave's first position of each digit goes
@@ -275,8 +268,8 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardA
         if (d < digits) {
             int o = before + a.ws.table[(int64_t)d * nb + blockIdx.x];
             for (int w = 0; w < kSortWaves; ++w) {
-                const int c = at[w][d];
-                at[w][d] = o;
+                const int c = at[(w << bits) + d];
+                at[(w << bits) + d] = o;
                 o += c;
             }
         }
@@ -294,9 +287,9 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardA
         }
         const int rank = lanes_below(same);
         int o = 0;
-        if (ok) o = at[wave][d];
+        if (ok) o = at[(wave << bits) + d];
         __builtin_amdgcn_wave_barrier();  // every lane has read before the first of a digit moves its place on
-        if (ok && rank == 0) at[wave][d] = o + __popcll(same);
+        if (ok && rank == 0) at[(wave << bits) + d] = o + __popcll(same);
         __builtin_amdgcn_wave_barrier();
         if (ok) {
             keys_out[o + rank] = key[r];
@@ -311,17 +304,32 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardA
 // Sums of a word that lies in the tile are written; the tile's part of one that
 // began before it goes to part 0 of the tile, of one that goes on behind it to
 // part 1 (to part 0 if it did both).
-template <typename T, int N>
-__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, const int32_t* keys, const int32_t* pos, int lanes,
-                                                        int tile, int tiles) {
-    const int g = blockIdx.x * (256 / lanes) + threadIdx.x / lanes, lane = threadIdx.x % lanes;
+// Whole: a group is whole waves, so its words are the same in every lane of a
+// wave and the branches on them are scalar.
+template <typename T, int N, bool Whole>
+__global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, const int32_t* __restrict__ keys,
+                                                        const int32_t* __restrict__ pos, int lanes, int tile, int tiles) {
+    const auto uniform = [](int x) { return Whole ? __builtin_amdgcn_readfirstlane(x) : x; };
+    const int g = uniform(blockIdx.x * (256 / lanes) + threadIdx.x / lanes), lane = threadIdx.x % lanes;
     if (g >= tiles) return;
     const int i0 = g * tile, i1 = min(a.n, i0 + tile);
-    const int before = i0 > 0 ? keys[i0 - 1] : -1, behind = i1 < a.n ? keys[i1] : a.V;
+    const int before = uniform(i0 > 0 ? keys[i0 - 1] : -1), behind = uniform(i1 < a.n ? keys[i1] : a.V);
     constexpr int kAhead = 8;
-    for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
+    for (int d = lane * N; d < a.D; d += lanes * N) {
         float s[N] = {};
-        int v = keys[i0];
+        const auto end_word = [&](int v, bool at_end) {  // the tile's last position of v is summed
+            const bool began = v == before, goes_on = at_end && v == behind;
+            if (began || goes_on) {
+                float* p = a.ws.parts + ((int64_t)g * 2 + (began ? 0 : 1)) * a.Dp + d;
+#pragma unroll
+                for (int e = 0; e < N; ++e) p[e] = s[e];
+            } else {
+                put_word<T, N>(a, v, d, s);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e] = 0.0f;
+        };
+        int v = uniform(keys[i0]);
         int kn[kAhead], pn[kAhead];  // the next round's words and positions
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -329,12 +337,12 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
             pn[u] = i0 + u < i1 ? pos[i0 + u] : 0;
         }
         for (int i = i0; i < i1 && v < a.V; i += kAhead) {
-            float x[kAhead][N];
+            typename Pack<T, N>::Raw x[kAhead];
             int k[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                k[u] = kn[u];
-                if (k[u] < a.V) Pack<T, N>::load((const T*)a.grad + (int64_t)pn[u] * a.gstride + d, x[u]);
+                k[u] = uniform(kn[u]);
+                if (k[u] < a.V) x[u] = Pack<T, N>::raw((const T*)a.grad + (int64_t)uniform(pn[u]) * a.gstride + d);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -344,38 +352,15 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (k[u] != v && v < a.V) {  // v ends here
-                    if (v == before) {
-                        float* p = a.ws.parts + (int64_t)g * 2 * a.Dp + d;
-#pragma unroll
-                        for (int e = 0; e < N; ++e) p[e] = s[e];
-                    } else if (i + u < i1 || v != behind) {
-                        put_word<T, N>(a, v, d, s);
-                    } else {
-                        float* p = a.ws.parts + ((int64_t)g * 2 + 1) * a.Dp + d;
-#pragma unroll
-                        for (int e = 0; e < N; ++e) p[e] = s[e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < N; ++e) s[e] = 0.0f;
-                }
-                if (k[u] < a.V) {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) s[e] += x[u][e];
-                }
+                if (k[u] != v && v < a.V) end_word(v, i + u >= i1);
                 v = k[u];
-            }
-        }
-        // the tile's last position was the group's last of a round of kAhead
-        if (v < a.V) {
-            float* p = a.ws.parts + ((int64_t)g * 2 + (v == before ? 0 : 1)) * a.Dp + d;
-            const bool whole = v != before && v != behind;
-            if (whole) put_word<T, N>(a, v, d, s);
-            else {
+                if (v < a.V) {
 #pragma unroll
-                for (int e = 0; e < N; ++e) p[e] = s[e];
+                    for (int e = 0; e < N; ++e) s[e] += Pack<T, N>::value(x[u], e);
+                }
             }
         }
+        if (v < a.V) end_word(v, true);  // the tile ended with a round
     }
 }
 
@@ -483,17 +468,18 @@ hipError_t backward_t(const EmbedBackwardArgs& a, hipStream_t st) {
     for (int q = 0; q < p.passes; ++q) {
         const int shift = q * p.bits, out = q & 1, digits = 1 << p.bits, scans = (digits + 3) / 4;
         int more = share();
-        embed_count_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, 0, st>>>(a, keys, p.blocks, shift, digits, f);
+        embed_count_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, digits * sizeof(int), st>>>(a, keys, p.blocks, shift, digits, f);
         more = share();
         embed_scan_kernel<<<dim3((unsigned)(scans + more)), 256, 0, st>>>(a, p.blocks, digits, scans, f);
         more = share();
-        embed_move_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, 0, st>>>(a, keys, pos, a.ws.keys[out], a.ws.pos[out],
-                                                                                     p.blocks, shift, p.bits, f);
+        embed_move_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, kSortWaves * digits * sizeof(int), st>>>(
+            a, keys, pos, a.ws.keys[out], a.ws.pos[out], p.blocks, shift, p.bits, f);
         keys = a.ws.keys[out];
         pos = a.ws.pos[out];
     }
     const dim3 grid((unsigned)((p.tiles + groups - 1) / groups));
-    embed_sum_kernel<T, N><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
+    if (lanes >= 64) embed_sum_kernel<T, N, true><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
+    else embed_sum_kernel<T, N, false><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
     embed_join_kernel<T, N><<<dim3((unsigned)p.tiles), kJoinThreads, 0, st>>>(a, keys, lanes, p.tile, p.tiles);
     return hipGetLastError();
 }
