@@ -263,12 +263,12 @@ __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operan
 }
 
 // Loss and lse of each row from its parts: workgroups of `rb` rows, 1024 / rb
-// threads to a row.
-__global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t rows_cap, int parts, int rb) {
+// threads to a row.  packed: the rows are pack_rows_kernel's.
+__global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t rows_cap, int parts, int rb, bool packed) {
     __shared__ float sm[1024], ss[1024];
     const int slices = 1024 / rb, row = threadIdx.x % rb, slice = threadIdx.x / rb;
     const int n = blockIdx.x * rb + row;
-    const int at = n < a.N ? a.ws.place[n] : -1;
+    const int at = n >= a.N ? -1 : packed ? a.ws.place[n] : has_target(a, n) ? n : -1;
     float m = kFarBelow, s = 0.0f;
     if (at >= 0)
         for (int p = slice; p < parts; p += slices) {
@@ -296,6 +296,188 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t row
         }
         a.loss[n] = loss;
         a.lse[n] = lse;
+    }
+}
+
+// ------------------------------------------------------------- few rows
+
+// Forward of at most 64 rows: bound by reading the table once.  A workgroup
+// takes 128 words, a wave 32 of them; the words go from memory straight to the
+// matrix cores' registers (two k steps ahead), fp32 ones split into planes on
+// the way, since each is used by one wave only.  The hidden states, which every
+// wave needs, go through LDS a k step at a time.  Nothing is packed before:
+// rows without a target are staged as zeros.
+constexpr int kFewRows = 64, kStreamWords = 128, kStreamK = 64;
+
+template <typename T>
+struct Raw8;  // eight elements as loaded
+template <>
+struct Raw8<uint16_t> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const uint16_t* p, int d, int D, bool wide) { v = load8_bits(p, d, D, wide); }
+    __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ void planes(bf16x8 (&b)[1]) const { b[0] = __builtin_bit_cast(bf16x8, v); }
+};
+template <>
+struct Raw8<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float* p, int d, int D, bool wide) { load8(p, d, D, wide, x); }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+    }
+    __device__ __forceinline__ void planes(bf16x8 (&b)[3]) const {
+        s16x8 t[3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint16_t h[3];
+            split_planes<3>(x[e], h);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) t[p][e] = (short)h[p];
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) b[p] = __builtin_bit_cast(bf16x8, t[p]);
+    }
+};
+
+template <typename T, int FN>
+__global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
+    constexpr int PL = sizeof(T) == 2 ? 1 : 3, kRows = FN * 16, kItems = (kRows * 8 + 255) / 256;
+    __shared__ __align__(16) uint16_t hs[2][PL][kRows][kStreamK];
+    __shared__ float sm[4][kRows], ss[4][kRows];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const bool hwide = rows_wide((const T*)a.hidden, a.hstride), wwide = rows_wide((const T*)a.weight, a.wstride);
+    const int v0 = blockIdx.x * kStreamWords + wave * 32;
+    const int steps = tiles_of(a.D, kStreamK);
+
+    // this thread's 16-byte chunks of the hidden states' step
+    const T* hrow[kItems];
+    bool hok[kItems];
+#pragma unroll
+    for (int q = 0; q < kItems; ++q) {
+        const int n = (q * 256 + threadIdx.x) / 8;
+        hok[q] = n < kRows && has_target(a, n);
+        hrow[q] = (const T*)a.hidden + (int64_t)(hok[q] ? n : 0) * a.hstride;
+    }
+    Raw8<T> hr[kItems];
+    const auto fetch_h = [&](int c) {
+#pragma unroll
+        for (int q = 0; q < kItems; ++q) {
+            const int d = c * kStreamK + (threadIdx.x & 7) * 8;
+            if (hok[q] && d < a.D) hr[q].load(hrow[q], d, a.D, hwide);
+            else hr[q].zero();
+        }
+    };
+    const auto stage_h = [&](int buf) {
+#pragma unroll
+        for (int q = 0; q < kItems; ++q) {
+            const int n = (q * 256 + threadIdx.x) / 8;
+            if (n >= kRows) continue;
+            bf16x8 b[PL];
+            hr[q].planes(b);
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+                *(bf16x8*)&hs[buf][p][n][((threadIdx.x & 7) ^ along_swz<8, false>(n)) * 8] = b[p];
+        }
+    };
+    const T* wrow[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+        wrow[f] = (const T*)a.weight + (int64_t)min(a.V - 1, v0 + f * 16 + (lane & 15)) * a.wstride;
+    struct Words {
+        Raw8<T> r[2][2];
+    } w0, w1;
+    const auto fetch_w = [&](Words& w, int c) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const int d = c * kStreamK + kk * 32 + (lane >> 4) * 8;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                if (d < a.D) w.r[f][kk].load(wrow[f], d, a.D, wwide);
+                else w.r[f][kk].zero();
+            }
+        }
+    };
+    f32x4v acc[2][FN] = {};
+    const auto step = [&](int c, Words& w) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes and reads
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (c + 1 < steps) stage_h((c + 1) & 1);
+        if (c + 2 < steps) fetch_h(c + 2);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8 b[PL][FN];
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const int n = j * 16 + (lane & 15);
+                    b[p][j] = *(const bf16x8*)&hs[c & 1][p][n][((kk * 4 + (lane >> 4)) ^ along_swz<8, false>(n)) * 8];
+                }
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                bf16x8 x[PL];
+                w.r[f][kk].planes(x);
+#pragma unroll
+                for (int sum = PL - 1; sum >= 0; --sum)
+#pragma unroll
+                    for (int pa = sum; pa >= 0; --pa)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j)
+                            acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[pa], b[sum - pa][j], acc[f][j], 0, 0, 0);
+            }
+        }
+        if (c + 2 < steps) fetch_w(w, c + 2);
+    };
+    fetch_w(w0, 0);
+    fetch_h(0);
+    stage_h(0);
+    if (steps > 1) {
+        fetch_h(1);
+        fetch_w(w1, 1);
+    }
+    for (int c = 0; c < steps; c += 2) {
+        step(c, w0);
+        if (c + 1 < steps) step(c + 1, w1);
+    }
+
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int n = j * 16 + (lane & 15);
+        const int t = has_target(a, n) ? a.targets[n] - v0 - (lane >> 4) * 4 : -1;
+        float m = kFarBelow, s = 0.0f;
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float z = acc[f][j][r] * a.scale;
+                acc[f][j][r] = z;
+                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) m = fmaxf(m, z);
+                if (t == f * 16 + r) a.ws.zt[n] = z;
+            }
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) s += ex2((acc[f][j][r] - m) * kLog2e);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (lane < 16) {
+            sm[wave][n] = m;
+            ss[wave][n] = s;
+        }
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < kRows && (int)threadIdx.x < a.N) {
+        const int n = threadIdx.x;
+        const float m = fmaxf(fmaxf(sm[0][n], sm[1][n]), fmaxf(sm[2][n], sm[3][n]));
+        float s = 0.0f;
+        for (int w = 0; w < 4; ++w) s += ss[w][n] * ex2((sm[w][n] - m) * kLog2e);
+        a.ws.parts[(int64_t)blockIdx.x * a.N + n] = make_float2(m, s);
     }
 }
 
@@ -519,6 +701,16 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
         a.loss = all.loss + r;
         a.lse = all.lse + r;
         a.grad_loss = nullptr;
+        if (a.N <= kFewRows) {
+            const unsigned wgs = (unsigned)tiles_of(a.V, kStreamWords);
+            if (a.N <= 16) head_stream_kernel<T, 1><<<dim3(wgs), 256, 0, st>>>(a);
+            else if (a.N <= 32) head_stream_kernel<T, 2><<<dim3(wgs), 256, 0, st>>>(a);
+            else head_stream_kernel<T, 4><<<dim3(wgs), 256, 0, st>>>(a);
+            head_join_kernel<<<dim3((unsigned)a.N), 1024, 0, st>>>(a, a.N, (int)wgs, 1, false);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            continue;
+        }
         hipError_t e = pack_rows<T>(a, cap, st);
         if (e != hipSuccess) return e;
         const bool large = use_large(a.V, a.N, Large::BM, Large::BN);
@@ -530,8 +722,8 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
             else run_parts<Small>(a, W, cap, v, nv, st);
         }
         const int parts = tiles_of(a.V, large ? Large::WM : Small::WM);
-        const int rb = a.N <= 64 ? 1 : 16;
-        head_join_kernel<<<dim3((unsigned)tiles_of(a.N, rb)), 1024, 0, st>>>(a, cap, parts, rb);
+        const int rb = 16;
+        head_join_kernel<<<dim3((unsigned)tiles_of(a.N, rb)), 1024, 0, st>>>(a, cap, parts, rb, true);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
