@@ -28,18 +28,30 @@ __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float
 __device__ __forceinline__ void store_elem(float* p, int64_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void store_elem(uint16_t* p, int64_t i, float v) { p[i] = bf16_bits(v); }
 
-// x as PL bf16 planes (gemm_tile.h).  A value whose first plane would round to
-// infinity takes the largest finite one, and the others carry the rest.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Two values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+}
+
+// x and y as PL bf16 planes (gemm_tile.h), each plane's pair packed.  A value
+// whose first plane would round to infinity starts from the largest finite
+// bf16 and the other planes carry the rest; a NaN comes back as the rest.
 template <int PL>
-__device__ __forceinline__ void split_planes(float x, uint16_t (&out)[PL]) {
-    out[0] = bf16_bits(x);
-    if (PL == 1) return;
-    if ((out[0] & 0x7FFF) == 0x7F80 && fabsf(x) < INFINITY) out[0] = (uint16_t)((out[0] & 0x8000) | 0x7F7F);
-    float rest = fabsf(x) < INFINITY ? x - bf16_value(out[0]) : 0.0f;  // inf, NaN: the first plane alone
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&out)[PL]) {
+    if (PL == 1) {
+        out[0] = bf16_pair(x, y);
+        return;
+    }
+    constexpr float kMost = 3.38953139e38f;  // the largest finite bf16
+    out[0] = bf16_pair(__builtin_amdgcn_fmed3f(x, -kMost, kMost), __builtin_amdgcn_fmed3f(y, -kMost, kMost));
 #pragma unroll
     for (int p = 1; p < PL; ++p) {
-        out[p] = bf16_bits(rest);
-        rest -= bf16_value(out[p]);
+        x -= __uint_as_float(out[p - 1] << 16);
+        y -= __uint_as_float(out[p - 1] & 0xFFFF0000u);
+        out[p] = bf16_pair(x, y);
     }
 }
 
@@ -80,13 +92,13 @@ __device__ __forceinline__ void pack_row(const float* src, int D, int Dp, bool w
     for (int d = lane * 8; d < Dp; d += lanes * 8) {
         float x[8];
         load8(src, d, D, wide, x);
-        u32x4 v[3] = {};
+        u32x4 v[3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint16_t b[3];
-            split_planes<3>(x[e], b);
+        for (int e = 0; e < 4; ++e) {
+            uint32_t b[3];
+            split_pair<3>(x[2 * e], x[2 * e + 1], b);
 #pragma unroll
-            for (int p = 0; p < 3; ++p) v[p][e >> 1] |= (uint32_t)b[p] << (16 * (e & 1));
+            for (int p = 0; p < 3; ++p) v[p][e] = b[p];
         }
 #pragma unroll
         for (int p = 0; p < 3; ++p) *(u32x4*)(dst + p * plane + d) = v[p];
@@ -327,13 +339,13 @@ struct Raw8<float> {
         for (int e = 0; e < 8; ++e) x[e] = 0.0f;
     }
     __device__ __forceinline__ void planes(bf16x8 (&b)[3]) const {
-        s16x8 t[3];
+        u32x4 t[3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint16_t h[3];
-            split_planes<3>(x[e], h);
+        for (int e = 0; e < 4; ++e) {
+            uint32_t h[3];
+            split_pair<3>(x[2 * e], x[2 * e + 1], h);
 #pragma unroll
-            for (int p = 0; p < 3; ++p) t[p][e] = (short)h[p];
+            for (int p = 0; p < 3; ++p) t[p][e] = h[p];
         }
 #pragma unroll
         for (int p = 0; p < 3; ++p) b[p] = __builtin_bit_cast(bf16x8, t[p]);
@@ -349,6 +361,10 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
     const bool hwide = rows_wide((const T*)a.hidden, a.hstride), wwide = rows_wide((const T*)a.weight, a.wstride);
     const int v0 = blockIdx.x * kStreamWords + wave * 32;
     const int steps = tiles_of(a.D, kStreamK);
+    // the width is walked in a circle from another step in every workgroup: rows
+    // of the table lie a power of two apart as often as not, and workgroups in
+    // step with one another would all ask the same memory channels
+    const int turn = (int)(blockIdx.x * 5u % (unsigned)steps);
 
     // this thread's 16-byte chunks of the hidden states' step
     const T* hrow[kItems];
@@ -361,6 +377,8 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
     }
     Raw8<T> hr[kItems];
     const auto fetch_h = [&](int c) {
+        c += turn;
+        c -= c >= steps ? steps : 0;
 #pragma unroll
         for (int q = 0; q < kItems; ++q) {
             const int d = c * kStreamK + (threadIdx.x & 7) * 8;
@@ -388,6 +406,8 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
         Raw8<T> r[2][2];
     } w0, w1;
     const auto fetch_w = [&](Words& w, int c) {
+        c += turn;
+        c -= c >= steps ? steps : 0;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             const int d = c * kStreamK + kk * 32 + (lane >> 4) * 8;
@@ -507,25 +527,27 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
         const float g = a.ws.gscale[n], lse = a.ws.lse[n];
 #pragma unroll
         for (int i = 0; i < Tile::FM; i += 2) {
-            union {
-                uint16_t h[PL][8];
-                u32x4 v[PL];
-            } out;
+            u32x4 out[PL];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int o = (i >> 1) * 32 + e;
-                const float z = acc[i + (e >> 2)][j][e & 3] * a.scale - lse;
-                float p = PL == 1 ? ex2(z * kLog2e) : expf(z);
-                if (o == t) p -= 1.0f;
-                uint16_t b[PL];
-                split_planes<PL>(vl + o < nv ? g * p : 0.0f, b);
+            for (int e = 0; e < 8; e += 2) {
+                float x[2];
 #pragma unroll
-                for (int pl = 0; pl < PL; ++pl) out.h[pl][e] = b[pl];
+                for (int q = 0; q < 2; ++q) {
+                    const int o = (i >> 1) * 32 + e + q;
+                    const float z = acc[i + (e >> 2)][j][(e & 3) + q] * a.scale - lse;
+                    float p = PL == 1 ? ex2(z * kLog2e) : expf(z);
+                    if (o == t) p -= 1.0f;
+                    x[q] = vl + o < nv ? g * p : 0.0f;
+                }
+                uint32_t b[PL];
+                split_pair<PL>(x[0], x[1], b);
+#pragma unroll
+                for (int pl = 0; pl < PL; ++pl) out[pl][e >> 1] = b[pl];
             }
             // the buffer's rows hold whole tiles: words behind the piece are zero
             uint16_t* dst = a.ws.G + (int64_t)n * a.plan.Vg + vl + (i >> 1) * 32;
 #pragma unroll
-            for (int pl = 0; pl < PL; ++pl) *(u32x4*)(dst + pl * plane) = out.v[pl];
+            for (int pl = 0; pl < PL; ++pl) *(u32x4*)(dst + pl * plane) = out[pl];
         }
     }
 }
