@@ -117,7 +117,7 @@ constexpr int kPackRows = 16;  // rows of a workgroup
 // targets before its own rows by itself (the targets of 2^16 rows are 256 KB
 // of L2 reads; a scan kernel before this one would cost a launch).
 template <typename T>
-__global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows_cap, int rows_per_wg) {
+__global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows_cap, int rows_per_wg, bool zero_rows) {
     __shared__ int wsum[4], base;
     const int r0 = blockIdx.x * rows_per_wg;
     int c = 0;
@@ -150,6 +150,7 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
             a.ws.place[mine] = at;
             if (ok) {
                 a.ws.target[at] = a.targets[mine];
+                a.ws.source[at] = mine;
                 if (a.grad_loss) {
                     a.ws.gscale[at] = a.scale * a.grad_loss[mine];
                     a.ws.lse[at] = a.lse_in[mine];
@@ -162,6 +163,15 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
             const int row = r1 + __builtin_ctzll(rest);
             pack_row((const T*)a.hidden + (int64_t)row * a.hstride, a.D, a.plan.Dp, wide,
                      a.ws.H + (int64_t)(before + k) * a.plan.Dp, rows_cap * a.plan.Dp, lane, 64);
+        }
+        if (zero_rows) {  // rows of grad_hidden without a target
+            uint64_t none = ~m;
+            if (r2 - r1 < 64) none &= (1ull << (r2 - r1)) - 1;
+            for (k = 0; none; none &= none - 1, ++k) {
+                if ((k & 3) != wave) continue;
+                T* o = (T*)a.ghidden + (int64_t)(r1 + __builtin_ctzll(none)) * a.ghstride;
+                for (int d = lane; d < a.D; d += 64) store_elem(o, d, 0.0f);
+            }
         }
         before += __popcll(m);
     }
@@ -554,11 +564,42 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
 
 // ------------------------------------------------------------- gradients
 
-// Partial sums of grad_hidden: split s of the piece's words, added to what the
-// pieces before left.
-template <typename Tile>
+// Four elements of a row of an output: 8 or 16 bytes at once where `wide` (the
+// rows start on as many); `add`: to what it holds; only `left` of them exist.
+__device__ __forceinline__ void put4(float* o, int left, bool wide, bool add, f32x4v x) {
+    if (wide && left >= 4) {
+        if (add) x += *(const f32x4v*)o;
+        *(f32x4v*)o = x;
+        return;
+    }
+    for (int r = 0; r < 4; ++r)
+        if (r < left) o[r] = add ? o[r] + x[r] : x[r];
+}
+__device__ __forceinline__ void put4(uint16_t* o, int left, bool wide, bool add, f32x4v x) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    if (wide && left >= 4) {
+        if (add) {
+            const u32x2 old = *(const u32x2*)o;
+            x += f32x4v{__uint_as_float(old[0] << 16), __uint_as_float(old[0] & 0xFFFF0000u), __uint_as_float(old[1] << 16),
+                        __uint_as_float(old[1] & 0xFFFF0000u)};
+        }
+        *(u32x2*)o = u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
+        return;
+    }
+    for (int r = 0; r < 4; ++r)
+        if (r < left) o[r] = bf16_bits(add ? bf16_value(o[r]) + x[r] : x[r]);
+}
+template <typename T>
+__device__ __forceinline__ bool rows_wide4(const T* p, int64_t stride) {
+    return (uintptr_t)p % (4 * sizeof(T)) == 0 && stride % 4 == 0;
+}
+
+// Split s of the piece's words: its share of grad_hidden, added to what the
+// pieces before left.  out: the last piece of an unsplit product writes the
+// rows themselves.
+template <typename T, typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Operand W, int64_t rows_cap, int nv, int splits,
-                                                                bool first) {
+                                                                bool first, bool out) {
     __shared__ __align__(1024) char lds[2 * Tile::Stage];
     const int count = *a.ws.count;
     const int tm = tiles_of(a.D, Tile::BM), tn = tiles_of(a.N, Tile::BN);
@@ -576,39 +617,38 @@ __global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Oper
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
     float* gh = a.ws.gh + (int64_t)s * a.N * a.plan.Dp;
+    const bool wide = out && rows_wide4((const T*)a.ghidden, a.ghstride);
 #pragma unroll
     for (int j = 0; j < Tile::FN; ++j) {
         const int n = rn + j * 16 + (lane & 15);
         if (n >= count) continue;
+        T* row = out ? (T*)a.ghidden + (int64_t)a.ws.source[n] * a.ghstride : nullptr;
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i) {
             const int d = rm + i * 16 + (lane >> 4) * 4;
             if (d >= a.plan.Dp) continue;
             f32x4v* o = (f32x4v*)(gh + (int64_t)n * a.plan.Dp + d);
-            *o = first ? acc[i][j] : *o + acc[i][j];
+            const f32x4v x = first ? acc[i][j] : *o + acc[i][j];
+            if (out) put4(row + d, a.D - d, wide, false, x);
+            else *o = x;
         }
     }
 }
 
-// grad_hidden: the splits' sums in order, one rounding; zero without a target.
+// grad_hidden of a split product: the splits' sums in order, one rounding; zero
+// without a target.
 template <typename T>
 __global__ __launch_bounds__(256) void head_ghidden_out_kernel(HeadArgs a, int splits) {
     const int n = blockIdx.x;
     const int at = a.ws.place[n];
     const int64_t stride = (int64_t)a.N * a.plan.Dp;
-    for (int d = threadIdx.x; d < a.D; d += 256) {
-        float s = 0.0f;
+    const bool wide = rows_wide4((const T*)a.ghidden, a.ghstride);
+    for (int d = threadIdx.x * 4; d < a.D; d += 1024) {
+        f32x4v s = {};
         if (at >= 0)
-            for (int q = 0; q < splits; ++q) s += a.ws.gh[q * stride + (int64_t)at * a.plan.Dp + d];
-        store_elem((T*)a.ghidden + (int64_t)n * a.ghstride, d, s);
+            for (int q = 0; q < splits; ++q) s += *(const f32x4v*)(a.ws.gh + q * stride + (int64_t)at * a.plan.Dp + d);
+        put4((T*)a.ghidden + (int64_t)n * a.ghstride + d, a.D - d, wide, false, s);
     }
-}
-
-template <typename T>
-__device__ __forceinline__ void put_gweight(const HeadArgs& a, int64_t v, int d, f32x4v x) {
-    T* o = (T*)a.gweight + v * a.gwstride + d;
-    for (int r = 0; r < 4; ++r)
-        if (d + r < a.D) store_elem(o, r, a.accumulate ? load_elem(o, r) + x[r] : x[r]);
 }
 
 // The piece's rows of grad_weight, or (splits > 1) partial sums of them over a
@@ -626,6 +666,7 @@ __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int6
     const int k0 = s * per, k1 = min(count, k0 + per);
     f32x4v acc[Tile::FM][Tile::FN] = {};
     Tile::run(hidden_operand(a, rows_cap, count), m0, grad_operand(a, rows_cap, count), n0, k0, k1, lds, acc);
+    const bool wide = rows_wide4((const T*)a.gweight, a.gwstride);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
@@ -638,7 +679,7 @@ __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int6
             const int d = rm + i * 16 + (lane >> 4) * 4;
             if (d >= a.plan.Dp) continue;
             if (splits > 1) *(f32x4v*)(a.ws.gw + ((int64_t)s * nv + v) * a.plan.Dp + d) = acc[i][j];
-            else put_gweight<T>(a, vp + v, d, acc[i][j]);
+            else put4((T*)a.gweight + (int64_t)(vp + v) * a.gwstride + d, a.D - d, wide, a.accumulate, acc[i][j]);
         }
     }
 }
@@ -646,10 +687,11 @@ __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int6
 template <typename T>
 __global__ __launch_bounds__(256) void head_gweight_out_kernel(HeadArgs a, int vp, int nv, int splits) {
     const int v = blockIdx.x;
+    const bool wide = rows_wide4((const T*)a.gweight, a.gwstride);
     for (int d = threadIdx.x * 4; d < a.D; d += 1024) {
         f32x4v s = {};
         for (int q = 0; q < splits; ++q) s += *(const f32x4v*)(a.ws.gw + ((int64_t)q * nv + v) * a.plan.Dp + d);
-        put_gweight<T>(a, vp + v, d, s);
+        put4((T*)a.gweight + (int64_t)(vp + v) * a.gwstride + d, a.D - d, wide, a.accumulate, s);
     }
 }
 
@@ -661,16 +703,46 @@ __global__ __launch_bounds__(256) void head_zero_kernel(HeadArgs a) {
 // ------------------------------------------------------------------ host
 
 constexpr int kMaxSplits = 64;
-constexpr int kFillTiles = 256;  // one tile to a CU
+constexpr int kCUs = 256;
 
-// Splits of the k axis that bring `tiles` workgroups up to about one per CU, at
-// least four k steps each.
-int pick_splits(int tiles, int ksteps) {
-    int s = kFillTiles / (tiles > 0 ? tiles : 1);
-    if (s > ksteps / 4) s = ksteps / 4;
-    if (s > kMaxSplits) s = kMaxSplits;
-    return s < 1 ? 1 : s;
+// How a product of m x n with k steps is cut: into large or small tiles, the k
+// axis into splits.  The cost is in k steps of a large tile: rounds of
+// workgroups over the chip, each its k steps and `ends` more for its first
+// loads and its epilogue; two small tiles (half a large bf16 tile's work
+// together) share a CU at four fifths of the large tile's rate.  Splits pay
+// for writing and reading their fp32 sums: a CU moves a large tile's in about
+// six k steps.
+struct Cut {
+    bool large;
+    int splits;
+};
+
+template <typename Large, typename Small>
+Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split, double ends) {
+    constexpr double kSmallStep = 2.0 * Small::BM * Small::BN / (Large::BM * Large::BN) / 0.8;
+    const int64_t steps = (k + Large::BK - 1) / Large::BK;
+    Cut best{true, 1};
+    double least = 1e300;
+    for (int large = 1; large >= 0; --large) {
+        const int64_t tiles = large ? (int64_t)tiles_of(m, Large::BM) * tiles_of(n, Large::BN)
+                                    : (int64_t)tiles_of(m, Small::BM) * tiles_of(n, Small::BN);
+        const int64_t slots = large ? kCUs : 2 * kCUs;
+        const double step = large ? 1.0 : kSmallStep;
+        for (int s = 1; s <= (may_split ? kMaxSplits : 1); ++s) {
+            if (s > 1 && (tiles * s > slots || steps / s < 4)) break;
+            const double rounds = (double)((tiles * s + slots - 1) / slots);
+            double cost = rounds * (((steps + s - 1) / s) + ends) * step;
+            if (s > 1) cost += 6.0 * step * (double)(tiles * s) / slots;
+            if (cost < least * 0.999) {
+                least = cost;
+                best = Cut{large != 0, s};
+            }
+        }
+    }
+    return best;
 }
+
+constexpr double kLogitEnds = 7, kSumEnds = 4;  // (cut_product) of the logits and of the gradients
 
 constexpr int64_t kPieceElems = 128ll << 20;   // of the logits' gradient
 constexpr int64_t kTableElems = 64ll << 20;    // of a packed piece of the table
@@ -683,13 +755,11 @@ bool reads_in_place(const void* p, int64_t stride, int D, int dtype) {
     return dtype == GR_BF16 && D % 8 == 0 && stride % 8 == 0 && stride <= kMaxTileStride && (uintptr_t)p % 16 == 0;
 }
 
-bool use_large(int64_t m, int64_t n, int bm, int bn) { return (int64_t)tiles_of(m, bm) * tiles_of(n, bn) >= 192; }
-
 template <typename T>
-hipError_t pack_rows(const HeadArgs& a, int64_t cap, hipStream_t st) {
+hipError_t pack_rows(const HeadArgs& a, int64_t cap, bool zero_rows, hipStream_t st) {
     int per = kPackRows;
     while (tiles_of(a.N, per) > 4096) per *= 2;  // the count before a workgroup's rows is quadratic in their number
-    pack_rows_kernel<T><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per);
+    pack_rows_kernel<T><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per, zero_rows);
     return hipGetLastError();
 }
 
@@ -733,9 +803,9 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
             if (e != hipSuccess) return e;
             continue;
         }
-        hipError_t e = pack_rows<T>(a, cap, st);
+        hipError_t e = pack_rows<T>(a, cap, false, st);
         if (e != hipSuccess) return e;
-        const bool large = use_large(a.V, a.N, Large::BM, Large::BN);
+        const bool large = cut_product<Large, Small>(a.V, a.N, a.D, false, kLogitEnds).large;
         const int step = reads_in_place(a.weight, a.wstride, a.D, dtype) ? a.V : a.plan.Vw;
         for (int v = 0; v < a.V; v += step) {
             const int nv = a.V - v < step ? a.V - v : step;
@@ -757,19 +827,16 @@ void run_grad(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, h
     head_grad_kernel<Tile><<<dim3((unsigned)(tiles_of(nv, Tile::BM) * tiles_of(a.N, Tile::BN))), Tile::NT, 0, st>>>(a, W, cap, v, nv);
 }
 
-template <typename Tile>
-int run_ghidden(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, hipStream_t st) {
+template <typename T, typename Tile>
+void run_ghidden(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, int splits, hipStream_t st) {
     const int tiles = tiles_of(a.D, Tile::BM) * tiles_of(a.N, Tile::BN);
-    // the first piece is the largest: its splits serve all
-    const int splits = pick_splits(tiles, tiles_of(a.V < a.plan.Vg ? a.V : a.plan.Vg, Tile::BK));
-    head_ghidden_kernel<Tile><<<dim3((unsigned)(tiles * splits)), Tile::NT, 0, st>>>(a, W, cap, nv, splits, v == 0);
-    return splits;
+    head_ghidden_kernel<T, Tile><<<dim3((unsigned)(tiles * splits)), Tile::NT, 0, st>>>(a, W, cap, nv, splits, v == 0,
+                                                                                       splits == 1 && v + nv == a.V);
 }
 
 template <typename T, typename Tile>
-void run_gweight(const HeadArgs& a, int64_t cap, int v, int nv, hipStream_t st) {
+void run_gweight(const HeadArgs& a, int64_t cap, int v, int nv, int splits, hipStream_t st) {
     const int tiles = tiles_of(a.D, Tile::BM) * tiles_of(nv, Tile::BN);
-    const int splits = pick_splits(tiles, tiles_of(a.N, Tile::BK));
     head_gweight_kernel<T, Tile><<<dim3((unsigned)(tiles * splits)), Tile::NT, 0, st>>>(a, cap, v, nv, splits);
     if (splits > 1) head_gweight_out_kernel<T><<<dim3((unsigned)nv), 256, 0, st>>>(a, v, nv, splits);
 }
@@ -783,26 +850,28 @@ hipError_t head_backward_t(const HeadArgs& a, int dtype, hipStream_t st) {
     typedef typename TileFor<T, true, true, true>::type WLarge;
     typedef typename TileFor<T, true, true, false>::type WSmall;
     const int64_t cap = a.plan.packed;
-    const hipError_t e = pack_rows<T>(a, cap, st);
-    if (e != hipSuccess) return e;
-    int splits = 1;
     const bool in_place = reads_in_place(a.weight, a.wstride, a.D, dtype);
     const int step = in_place || a.plan.Vg < a.plan.Vw ? a.plan.Vg : a.plan.Vw;
+    // grad_hidden's cut serves all pieces (their sums meet): the first is the largest
+    const Cut hc = cut_product<HLarge, HSmall>(a.D, a.N, a.V < step ? a.V : step, true, kSumEnds);
+    const hipError_t e = pack_rows<T>(a, cap, a.ghidden && hc.splits == 1, st);
+    if (e != hipSuccess) return e;
     for (int v = 0; v < a.V; v += step) {
         const int nv = a.V - v < step ? a.V - v : step;
         const Operand W = words_operand<T>(a, v, nv, dtype, st);
-        if (use_large(nv, a.N, ZLarge::BM, ZLarge::BN)) run_grad<ZLarge>(a, W, cap, v, nv, st);
+        if (cut_product<ZLarge, ZSmall>(nv, a.N, a.D, false, kLogitEnds).large) run_grad<ZLarge>(a, W, cap, v, nv, st);
         else run_grad<ZSmall>(a, W, cap, v, nv, st);
         if (a.ghidden) {
-            if (use_large(a.D, a.N, HLarge::BM, HLarge::BN)) splits = run_ghidden<HLarge>(a, W, cap, v, nv, st);
-            else splits = run_ghidden<HSmall>(a, W, cap, v, nv, st);
+            if (hc.large) run_ghidden<T, HLarge>(a, W, cap, v, nv, hc.splits, st);
+            else run_ghidden<T, HSmall>(a, W, cap, v, nv, hc.splits, st);
         }
         if (a.gweight) {
-            if (use_large(a.D, nv, WLarge::BM, WLarge::BN)) run_gweight<T, WLarge>(a, cap, v, nv, st);
-            else run_gweight<T, WSmall>(a, cap, v, nv, st);
+            const Cut c = cut_product<WLarge, WSmall>(a.D, nv, a.N, true, kSumEnds);
+            if (c.large) run_gweight<T, WLarge>(a, cap, v, nv, c.splits, st);
+            else run_gweight<T, WSmall>(a, cap, v, nv, c.splits, st);
         }
     }
-    if (a.ghidden) head_ghidden_out_kernel<T><<<dim3((unsigned)a.N), 256, 0, st>>>(a, splits);
+    if (a.ghidden && hc.splits > 1) head_ghidden_out_kernel<T><<<dim3((unsigned)a.N), 256, 0, st>>>(a, hc.splits);
     return hipGetLastError();
 }
 
@@ -822,10 +891,12 @@ HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool
     p.parts = (vocab + 63) / 64 * (int64_t)p.part_rows;  // the narrowest wave: 64 words
     if (backward) {
         const int64_t vg = kPieceElems / p.planes / max_rows / kWordTile * kWordTile;
-        p.Vg = (int32_t)(vg < kWordTile ? kWordTile : (vg < words ? vg : words));
+        const int64_t most_words = vg < kWordTile ? kWordTile : (vg < words ? vg : words);
+        const int64_t pieces = (words + most_words - 1) / most_words;  // of about the same size
+        p.Vg = (int32_t)round_up((words + pieces - 1) / pieces, kWordTile);
         p.G = (int64_t)p.planes * max_rows * p.Vg;
-        // a split product has at most kFillTiles tiles in all (pick_splits)
-        const int64_t most = (int64_t)kFillTiles * 256 * 256;
+        // a split product has at most one round of tiles (cut_product)
+        const int64_t most = (int64_t)kCUs * 256 * 256;
         const int64_t h = max_rows * p.Dp, w = (int64_t)p.Vg * p.Dp;
         p.gh = h > most ? h : (h * kMaxSplits < most ? h * kMaxSplits : most);
         p.gw = w * kMaxSplits < most ? w * kMaxSplits : most;

@@ -67,6 +67,7 @@ HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool
 struct HeadSpace {
     int32_t* count;    // [1] rows with a target
     int32_t* target;   // [packed row] its target
+    int32_t* source;   // [packed row] its row
     int32_t* place;    // [row] its packed row, -1 without a target
     float* gscale;     // [packed row] scale * grad_loss
     float* lse;        // [packed row]

@@ -199,7 +199,7 @@ extern "C" void gr_embed_free(gr_embed* h) {
 
 static void head_release(gr_head* h) {
     const gr::HeadSpace& w = h->ws;
-    void* all[] = {w.count, w.target, w.place, w.gscale, w.lse, w.zt, w.H, w.parts, w.W, w.G, w.gh, w.gw};
+    void* all[] = {w.count, w.target, w.source, w.place, w.gscale, w.lse, w.zt, w.H, w.parts, w.W, w.G, w.gh, w.gw};
     for (void* p : all) (void)hipFree(p);
     delete h;
 }
@@ -221,6 +221,7 @@ extern "C" gr_status gr_head_init(const gr_head_config* cfg, gr_stream stream, g
     gr::HeadSpace& w = h->ws;
     hipError_t e = dalloc(&w.count, 1);
     if (e == hipSuccess) e = dalloc(&w.target, p.packed);
+    if (e == hipSuccess) e = dalloc(&w.source, p.packed);
     if (e == hipSuccess) e = dalloc(&w.place, p.packed);
     if (e == hipSuccess) e = dalloc(&w.zt, p.packed);
     if (e == hipSuccess) e = dalloc(&w.H, (size_t)p.planes * p.packed * p.Dp);
