@@ -72,6 +72,11 @@ struct GemmTile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, PL = PL_;
     static constexpr int NT = (BM / WM) * (BN / WN) * 64;
     static constexpr int FM = WM / 16, FN = WN / 16;
+    // the waves take turns (see turns()): eight waves, two to a SIMD, whose "across"
+    // fragments take twice the LDS reads of "along" ones.  Measured at 2,048 x
+    // 16,384 x 7,424 (grad_weight's) 1,235 TFLOP/s against 1,094 in step, at
+    // 32,768 x 7,424 x 2,048 (the logits', both "along") 1,160 against 1,253.
+    static constexpr bool kTurns = AAcross && NT == 512;
     static constexpr bool kPerm = !AAcross;  // rows of A are interleaved (frag_row)
     static constexpr int ABytes = BM * BK * 2, BBytes = BN * BK * 2;  // a plane's
     static constexpr int Stage = PL * (ABytes + BBytes);
@@ -184,13 +189,16 @@ struct GemmTile {
         }
     }
 
-    // Waits for this wave's loads into LDS and its reads of it, then for the
-    // workgroup's.
-    static __device__ __forceinline__ void stage_barrier() {
+    // Waits for this wave's reads of LDS, and for its loads into LDS too if
+    // `loads`, then for the workgroup's.
+    static __device__ __forceinline__ void stage_barrier(bool loads) {
+        __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        if (loads) __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        else __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     // acc += the tile at rows m0 of A and n0 of B, k in [k0, k1).  lds: two
@@ -202,21 +210,87 @@ struct GemmTile {
         if (k0 >= k1) return;
         Fetch<BM, AAcross, kPerm> fa(A, m0, k0);
         Fetch<BN, BAcross, false> fb(B, n0, k0);
-        char* wave_lds = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
-        fa(wave_lds, k1 - k0);
-        fb(wave_lds + PL * ABytes, k1 - k0);
-        stage_barrier();
-        int stage = 0;
-        for (int k = k0; k < k1; k += BK) {
-            const int next = Stage - stage;
-            if (k + BK < k1) {
-                fa(wave_lds + next, k1 - k - BK);
-                fb(wave_lds + next + PL * ABytes, k1 - k - BK);
-            }
-            multiply(lds + stage, acc);
-            stage_barrier();
-            stage = next;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        char* wave_lds = lds + wave * 1024;
+        const int steps = (k1 - k0 + BK - 1) / BK;
+        const auto load = [&](int i) {
+            char* to = wave_lds + (i & 1) * Stage;
+            fa(to, k1 - k0 - i * BK);
+            fb(to + PL * ABytes, k1 - k0 - i * BK);
+        };
+        load(0);
+        if (kTurns) turns(lds, steps, wave >= NT / 128, load, acc);
+        else together(lds, steps, load, acc);
+    }
+
+    // All waves in step: the next step's loads are issued at the start of a
+    // step, whose matrix instructions hide them.
+    template <typename Load>
+    static __device__ __forceinline__ void together(const char* lds, int steps, const Load& load, f32x4v (&acc)[FM][FN]) {
+        for (int i = 0; i < steps; ++i) {
+            stage_barrier(true);
+            if (i + 1 < steps) load(i + 1);
+            __builtin_amdgcn_s_setprio(1);
+            multiply(lds + (i & 1) * Stage, acc);
+            __builtin_amdgcn_s_setprio(0);
         }
+    }
+
+    // The two waves of a SIMD take turns: while one reads its fragments of a
+    // whole step, the other's matrix instructions run.  Half of the waves
+    // (`second`) are a phase behind; phase 2i is the first half's reads of step
+    // i and the second half's products of step i - 1, phase 2i + 1 the other way
+    // round.  Step i + 1 is loaded by all in phase 2i (its stage was last read
+    // in phase 2i - 1) and waited for at the end of phase 2i + 1.
+    template <typename Load>
+    static __device__ __forceinline__ void turns(const char* lds, int steps, bool second, const Load& load,
+                                                 f32x4v (&acc)[FM][FN]) {
+        const int wave = threadIdx.x >> 6;
+        const int rm = (wave / (BN / WN)) * WM, rn = (wave % (BN / WN)) * WN;
+        constexpr int kHalves = BK / 32;
+        stage_barrier(true);
+        if (second) {
+            if (steps > 1) load(1);
+            stage_barrier(false);
+        }
+        for (int i = 0; i < steps; ++i) {
+            const char* st = lds + (i & 1) * Stage;
+            if (!second && i + 1 < steps) load(i + 1);
+            bf16x8 a[kHalves][PL][FM], b[kHalves][PL][FN];
+#pragma unroll
+            for (int kk = 0; kk < kHalves; ++kk)
+#pragma unroll
+                for (int pl = 0; pl < PL; ++pl) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) {
+                        const char* t = st + PL * ABytes + pl * BBytes;
+                        b[kk][pl][j] = BAcross ? frag_across<BN>(t, rn, j, kk) : frag_along<false>(t, rn, j, kk);
+                    }
+#pragma unroll
+                    for (int q = 0; q < FM; ++q) {
+                        const char* t = st + pl * ABytes;
+                        a[kk][pl][q] = AAcross ? frag_across<BM>(t, rm, q, kk) : frag_along<kPerm>(t, rm, q, kk);
+                    }
+                }
+            stage_barrier(second);
+            if (second && i + 2 < steps) load(i + 2);
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int kk = 0; kk < kHalves; ++kk)
+#pragma unroll
+                for (int sum = PL - 1; sum >= 0; --sum)
+#pragma unroll
+                    for (int pa = sum; pa >= 0; --pa)
+#pragma unroll
+                        for (int q = 0; q < FM; ++q)
+#pragma unroll
+                            for (int j = 0; j < FN; ++j)
+                                acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[kk][pa][q], b[kk][sum - pa][j], acc[q][j],
+                                                                                    0, 0, 0);
+            __builtin_amdgcn_s_setprio(0);
+            stage_barrier(!second);
+        }
+        if (!second) stage_barrier(false);
     }
 };
 
