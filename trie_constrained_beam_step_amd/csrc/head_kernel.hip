@@ -252,32 +252,49 @@ __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operan
     if (rm >= nv) return;
     const int vl = vp + rm + (lane >> 4) * 8;  // word of acc[0][j][0]
     const int part = (vp + rm) / Tile::WM;
+    const float c = a.scale * kLog2e;
 #pragma unroll
     for (int j = 0; j < Tile::FN; ++j) {
         const int n = rn + j * 16 + (lane & 15);
         const int t = n < count ? a.ws.target[n] - vl : -1;
+        if (__ballot(t >= 0 && t < Tile::WM) == 0) continue;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if ((i >> 1) * 32 + (i & 1) * 4 + r == t) a.ws.zt[n] = acc[i][j][r] * a.scale;
+    }
+    // from here on in units of log 2: y = z log2 e
+#pragma unroll
+    for (int i = 0; i < Tile::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] *= c;
+    if (vp + rm + Tile::WM > a.V) {  // words behind the table take no part
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (vl + (i >> 1) * 32 + (i & 1) * 4 + r >= a.V)
+#pragma unroll
+                    for (int j = 0; j < Tile::FN; ++j) acc[i][j][r] = kFarBelow;
+    }
+#pragma unroll
+    for (int j = 0; j < Tile::FN; ++j) {
+        const int n = rn + j * 16 + (lane & 15);
         float m = kFarBelow;
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int o = (i >> 1) * 32 + (i & 1) * 4 + r;
-                const float z = acc[i][j][r] * a.scale;
-                acc[i][j][r] = z;
-                if (vl + o < a.V) m = fmaxf(m, z);
-                if (o == t) a.ws.zt[n] = z;
-            }
+            for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[i][j][r]);
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int o = (i >> 1) * 32 + (i & 1) * 4 + r;
-                const float e = ex2((acc[i][j][r] - m) * kLog2e);
-                if (vl + o < a.V) s += e;
-            }
+            for (int r = 0; r < 4; ++r) s += ex2(acc[i][j][r] - m);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (lane < 16 && n < count) a.ws.parts[(int64_t)part * rows_cap + n] = make_float2(m, s);
@@ -296,7 +313,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t row
         for (int p = slice; p < parts; p += slices) {
             const float2 x = a.ws.parts[(int64_t)p * rows_cap + at];
             const float hi = fmaxf(m, x.x);
-            s = s * ex2((m - hi) * kLog2e) + x.y * ex2((x.x - hi) * kLog2e);
+            s = s * ex2(m - hi) + x.y * ex2(x.x - hi);
             m = hi;
         }
     sm[threadIdx.x] = m;
@@ -306,14 +323,14 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t row
         if (slice < half) {
             const int o = threadIdx.x + half * rb;
             const float hi = fmaxf(sm[threadIdx.x], sm[o]);
-            ss[threadIdx.x] = ss[threadIdx.x] * ex2((sm[threadIdx.x] - hi) * kLog2e) + ss[o] * ex2((sm[o] - hi) * kLog2e);
+            ss[threadIdx.x] = ss[threadIdx.x] * ex2(sm[threadIdx.x] - hi) + ss[o] * ex2(sm[o] - hi);
             sm[threadIdx.x] = hi;
         }
     }
     if (slice == 0 && n < a.N) {
         float lse = 0.0f, loss = 0.0f;
         if (at >= 0) {
-            lse = sm[row] + logf(ss[row]);
+            lse = (float)(kLn2 * ((double)sm[row] + (double)log2f(ss[row])));
             loss = lse - a.ws.zt[at];
         }
         a.loss[n] = loss;
@@ -482,10 +499,9 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
         for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float z = acc[f][j][r] * a.scale;
-                acc[f][j][r] = z;
-                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) m = fmaxf(m, z);
-                if (t == f * 16 + r) a.ws.zt[n] = z;
+                if (t == f * 16 + r) a.ws.zt[n] = acc[f][j][r] * a.scale;
+                acc[f][j][r] *= a.scale * kLog2e;
+                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) m = fmaxf(m, acc[f][j][r]);
             }
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
@@ -493,7 +509,7 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
         for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) s += ex2((acc[f][j][r] - m) * kLog2e);
+                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) s += ex2(acc[f][j][r] - m);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (lane < 16) {
@@ -506,7 +522,7 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
         const int n = threadIdx.x;
         const float m = fmaxf(fmaxf(sm[0][n], sm[1][n]), fmaxf(sm[2][n], sm[3][n]));
         float s = 0.0f;
-        for (int w = 0; w < 4; ++w) s += ss[w][n] * ex2((sm[w][n] - m) * kLog2e);
+        for (int w = 0; w < 4; ++w) s += ss[w][n] * ex2(sm[w][n] - m);
         a.ws.parts[(int64_t)blockIdx.x * a.N + n] = make_float2(m, s);
     }
 }
@@ -529,12 +545,15 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
     const int vl = rm + (lane >> 4) * 8;
     const int64_t plane = rows_cap * a.plan.Vg;
+    const float c = a.scale * kLog2e;
+    const bool whole = rm + Tile::WM <= nv;
 #pragma unroll
     for (int j = 0; j < Tile::FN; ++j) {
         const int n = rn + j * 16 + (lane & 15);
         if (n >= count) continue;
         const int t = a.ws.target[n] - vp - vl;
-        const float g = a.ws.gscale[n], lse = a.ws.lse[n];
+        const float g = a.ws.gscale[n], lse2 = a.ws.lse[n] * kLog2e;
+        const bool hit = __ballot(t >= 0 && t < Tile::WM) != 0;
 #pragma unroll
         for (int i = 0; i < Tile::FM; i += 2) {
             u32x4 out[PL];
@@ -544,10 +563,9 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int o = (i >> 1) * 32 + e + q;
-                    const float z = acc[i + (e >> 2)][j][(e & 3) + q] * a.scale - lse;
-                    float p = PL == 1 ? ex2(z * kLog2e) : expf(z);
-                    if (o == t) p -= 1.0f;
-                    x[q] = vl + o < nv ? g * p : 0.0f;
+                    float p = ex2(fmaf(acc[i + (e >> 2)][j][(e & 3) + q], c, -lse2));
+                    if (hit && o == t) p -= 1.0f;
+                    x[q] = whole || vl + o < nv ? g * p : 0.0f;
                 }
                 uint32_t b[PL];
                 split_pair<PL>(x[0], x[1], b);
@@ -700,6 +718,102 @@ __global__ __launch_bounds__(256) void head_zero_kernel(HeadArgs a) {
     for (int d = threadIdx.x; d < a.D; d += 256) store_elem((T*)a.gweight + (int64_t)blockIdx.x * a.gwstride, d, 0.0f);
 }
 
+// ------------------------------------------------------------ small problems
+
+// The whole backward in one launch, where several would cost more than the
+// work: a workgroup takes 16 rows of grad_hidden or 16 rows of grad_weight,
+// computes the slab of G it needs (so each logit is computed twice) into LDS in
+// fp32 and multiplies it.  fp32 matrix instructions throughout, bf16 elements
+// widened; no rounding of G.  A k of four is spread over a lane's four
+// consecutive elements: both operands agree on which.
+constexpr int kSmallMost = 512;  // rows and words at most: their share of G is 33 KB of LDS
+
+__device__ __forceinline__ f32x4v load4_wide(const float* p) { return *(const f32x4v*)p; }
+__device__ __forceinline__ f32x4v load4_wide(const uint16_t* p) {
+    const uint2 v = *(const uint2*)p;
+    return f32x4v{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                  __uint_as_float(v.y & 0xFFFF0000u)};
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, int row_wgs) {
+    extern __shared__ __align__(16) float gs[];  // [16][pitch]: rows (or words) x words (or rows)
+    __shared__ bool there[kSmallMost];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
+    const bool rows = (int)blockIdx.x < row_wgs;  // grad_hidden's workgroup
+    const int r0 = rows ? blockIdx.x * 16 : 0, w0 = rows ? 0 : (blockIdx.x - row_wgs) * 16;
+    const int others = rows ? a.V : a.N;  // the length of the second product
+    const int pitch = (others + 15) / 16 * 16 + 4;
+    const bool hwide = rows_wide4((const T*)a.hidden, a.hstride), wwide = rows_wide4((const T*)a.weight, a.wstride);
+    const float c = a.scale * kLog2e;
+
+    // Loads are from clamped places and unconditional (a branch around each would
+    // leave one in flight); what does not exist is zeroed behind them.
+    for (int o0 = wave * 16; o0 < others; o0 += 64) {
+        const int v = (rows ? o0 : w0) + li, n = (rows ? r0 : o0) + li;
+        const bool vin = v < a.V, nin = has_target(a, n);
+        const T* wp = (const T*)a.weight + (int64_t)(vin ? v : 0) * a.wstride;
+        const T* hp = (const T*)a.hidden + (int64_t)(nin ? n : 0) * a.hstride;
+        const float g = nin ? a.scale * a.grad_loss[n] : 0.0f, lse2 = nin ? a.lse_in[n] * kLog2e : 0.0f;
+        const int t = nin ? a.targets[n] - (v - li) : -1;
+        f32x4v acc = {};
+        int d0 = 0;
+        if (hwide && wwide) {
+#pragma unroll 4
+            for (; d0 + 16 <= a.D; d0 += 16) {
+                const f32x4v x = load4_wide(wp + d0 + lk * 4), y = load4_wide(hp + d0 + lk * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin ? x[e] : 0.0f, nin ? y[e] : 0.0f, acc, 0, 0, 0);
+            }
+        }
+        for (; d0 < a.D; d0 += 16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = d0 + lk * 4 + e, at = min(d, a.D - 1);
+                const float x = load_elem(wp, at), y = load_elem(hp, at);
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin && d < a.D ? x : 0.0f, nin && d < a.D ? y : 0.0f, acc, 0, 0, 0);
+            }
+        }
+        // acc[r]: word 4*lk + r of the tile, row li
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int w = lk * 4 + r;
+            float p = ex2(fmaf(acc[r], c, -lse2));
+            if (w == t) p -= 1.0f;
+            const float x = nin && v - li + w < a.V ? g * p : 0.0f;
+            if (rows) gs[li * pitch + o0 + w] = x;
+            else gs[w * pitch + o0 + li] = x;
+        }
+        // which rows of the second product's left side exist
+        if (lk == 0) there[o0 + li] = rows ? vin : nin;
+    }
+    __syncthreads();
+    const int mine = (rows ? r0 : w0) + li;  // this lane's row of the output
+    const bool stored = mine < (rows ? a.N : a.V);
+    const bool zero = rows && !has_target(a, mine);
+    T* out = rows ? (T*)a.ghidden + (int64_t)mine * a.ghstride : (T*)a.gweight + (int64_t)mine * a.gwstride;
+    const bool owide = rows ? rows_wide4((const T*)a.ghidden, a.ghstride) : rows_wide4((const T*)a.gweight, a.gwstride);
+    const T* left = rows ? (const T*)a.weight : (const T*)a.hidden;
+    const int64_t lstride = rows ? a.wstride : a.hstride;
+    const int padded = (others + 15) / 16 * 16;
+    for (int d0 = wave * 16; d0 < a.D; d0 += 64) {
+        f32x4v acc = {};
+        const T* col = left + min(d0 + li, a.D - 1);
+#pragma unroll 2
+        for (int k0 = 0; k0 < padded; k0 += 16) {
+#pragma unroll
+            for (int q = 0; q < 16; q += 4) {
+                const int k = k0 + q + lk;
+                const float x = load_elem(col, (int64_t)min(k, others - 1) * lstride);
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(there[k] ? x : 0.0f, gs[li * pitch + k], acc, 0, 0, 0);
+            }
+        }
+        const int od = d0 + lk * 4;
+        if (stored && od < a.D) put4(out + od, a.D - od, owide, !rows && a.accumulate, zero ? f32x4v{} : acc);
+    }
+}
+
 // ------------------------------------------------------------------ host
 
 constexpr int kMaxSplits = 64;
@@ -814,7 +928,8 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
             else run_parts<Small>(a, W, cap, v, nv, st);
         }
         const int parts = tiles_of(a.V, large ? Large::WM : Small::WM);
-        const int rb = 16;
+        int rb = 256;  // four threads to a row, more where it has many parts
+        while (rb > 16 && parts > 8 * (1024 / rb)) rb /= 2;
         head_join_kernel<<<dim3((unsigned)tiles_of(a.N, rb)), 1024, 0, st>>>(a, cap, parts, rb, true);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -841,8 +956,25 @@ void run_gweight(const HeadArgs& a, int64_t cap, int v, int nv, int splits, hipS
     if (splits > 1) head_gweight_out_kernel<T><<<dim3((unsigned)nv), 256, 0, st>>>(a, v, nv, splits);
 }
 
+// One launch: up to kSmallMost rows and words, and no more work for the busiest
+// workgroup than the other way's launches cost.  Loss and backward together:
+// fp32 256 x 256 x 256 70 us against 102, 500 x 500 x 256 103 against 107 (three
+// planes cost the other way more); bf16 48 x 48 x 64 36 against 48, 256 x 256 x
+// 256 56 against 50.
+bool small_backward(const HeadArgs& a, int dtype) {
+    const int64_t most = a.N > a.V ? a.N : a.V;
+    return most <= kSmallMost && most * a.D <= (dtype == GR_BF16 ? 32 << 10 : 128 << 10);
+}
+
 template <typename T>
 hipError_t head_backward_t(const HeadArgs& a, int dtype, hipStream_t st) {
+    if (small_backward(a, dtype)) {
+        const int row_wgs = a.ghidden ? tiles_of(a.N, 16) : 0, word_wgs = a.gweight ? tiles_of(a.V, 16) : 0;
+        const int most = a.N > a.V ? a.N : a.V;
+        const size_t lds = 16 * (size_t)(tiles_of(most, 16) * 16 + 4) * sizeof(float);
+        head_small_backward_kernel<T><<<dim3((unsigned)(row_wgs + word_wgs)), 256, lds, st>>>(a, row_wgs);
+        return hipGetLastError();
+    }
     typedef typename TileFor<T, false, false, true>::type ZLarge;
     typedef typename TileFor<T, false, false, false>::type ZSmall;
     typedef typename TileFor<T, true, false, true>::type HLarge;

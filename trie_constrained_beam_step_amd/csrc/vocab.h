@@ -73,7 +73,7 @@ struct HeadSpace {
     float* lse;        // [packed row]
     float* zt;         // [packed row] the target's logit
     uint16_t* H;       // [planes][rows][Dp] packed hidden states
-    float2* parts;     // [parts of the vocabulary][rows] max and sum of exp(z - max)
+    float2* parts;     // [parts of the vocabulary][rows] max and sum of 2^(y - max), y = z log2 e
     uint16_t* W;       // [planes][Vw][Dp] a piece of the table, where it cannot be read as it lies
     uint16_t* G;       // [planes][rows][Vg] a piece of the logits' gradient
     float* gh;         // [splits][rows][Dp] partial sums of grad_hidden
