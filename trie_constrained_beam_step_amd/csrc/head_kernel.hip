@@ -829,28 +829,26 @@ constexpr int kCUs = 256;
 struct Cut {
     bool large;
     int splits;
+    double cost;
 };
+constexpr int kMostRounds = 3;  // of a split product
 
 template <typename Large, typename Small>
 Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split, double ends) {
     constexpr double kSmallStep = 2.0 * Small::BM * Small::BN / (Large::BM * Large::BN) / 0.8;
     const int64_t steps = (k + Large::BK - 1) / Large::BK;
-    Cut best{true, 1};
-    double least = 1e300;
+    Cut best{true, 1, 1e300};
     for (int large = 1; large >= 0; --large) {
         const int64_t tiles = large ? (int64_t)tiles_of(m, Large::BM) * tiles_of(n, Large::BN)
                                     : (int64_t)tiles_of(m, Small::BM) * tiles_of(n, Small::BN);
         const int64_t slots = large ? kCUs : 2 * kCUs;
         const double step = large ? 1.0 : kSmallStep;
         for (int s = 1; s <= (may_split ? kMaxSplits : 1); ++s) {
-            if (s > 1 && (tiles * s > slots || steps / s < 4)) break;
+            if (s > 1 && (tiles * s > kMostRounds * slots || steps / s < 4)) break;
             const double rounds = (double)((tiles * s + slots - 1) / slots);
             double cost = rounds * (((steps + s - 1) / s) + ends) * step;
             if (s > 1) cost += 6.0 * step * (double)(tiles * s) / slots;
-            if (cost < least * 0.999) {
-                least = cost;
-                best = Cut{large != 0, s};
-            }
+            if (cost < best.cost * 0.999) best = Cut{large != 0, s, cost};
         }
     }
     return best;
@@ -858,7 +856,7 @@ Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split, double ends) {
 
 constexpr double kLogitEnds = 7, kSumEnds = 4;  // (cut_product) of the logits and of the gradients
 
-constexpr int64_t kPieceElems = 128ll << 20;   // of the logits' gradient
+constexpr int64_t kPieceElems = 256ll << 20;   // of the logits' gradient at most (512 MB)
 constexpr int64_t kTableElems = 64ll << 20;    // of a packed piece of the table
 constexpr int64_t kPartRows = 65536;           // rows of a forward pass
 constexpr int kWordTile = 256;                 // pieces are whole tiles of any shape
@@ -966,6 +964,20 @@ bool small_backward(const HeadArgs& a, int dtype) {
     return most <= kSmallMost && most * a.D <= (dtype == GR_BF16 ? 32 << 10 : 128 << 10);
 }
 
+// Cost of the three products of a piece of `words` words.
+template <typename T>
+double piece_cost(int64_t rows, int64_t words, int64_t dim) {
+    typedef typename TileFor<T, false, false, true>::type ZLarge;
+    typedef typename TileFor<T, false, false, false>::type ZSmall;
+    typedef typename TileFor<T, true, false, true>::type HLarge;
+    typedef typename TileFor<T, true, false, false>::type HSmall;
+    typedef typename TileFor<T, true, true, true>::type WLarge;
+    typedef typename TileFor<T, true, true, false>::type WSmall;
+    return cut_product<ZLarge, ZSmall>(words, rows, dim, false, kLogitEnds).cost +
+           cut_product<HLarge, HSmall>(dim, rows, words, true, kSumEnds).cost +
+           cut_product<WLarge, WSmall>(dim, words, rows, true, kSumEnds).cost;
+}
+
 template <typename T>
 hipError_t head_backward_t(const HeadArgs& a, int dtype, hipStream_t st) {
     if (small_backward(a, dtype)) {
@@ -1024,11 +1036,23 @@ HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool
     if (backward) {
         const int64_t vg = kPieceElems / p.planes / max_rows / kWordTile * kWordTile;
         const int64_t most_words = vg < kWordTile ? kWordTile : (vg < words ? vg : words);
-        const int64_t pieces = (words + most_words - 1) / most_words;  // of about the same size
-        p.Vg = (int32_t)round_up((words + pieces - 1) / pieces, kWordTile);
+        // the fewest pieces or up to four more, whichever fills the chip best
+        const int64_t fewest = (words + most_words - 1) / most_words;
+        double least = 1e300;
+        for (int64_t pieces = fewest; pieces <= fewest + 4; ++pieces) {
+            const int64_t vg = round_up((words + pieces - 1) / pieces, kWordTile), last = words - (words - 1) / vg * vg;
+            const auto cost = [&](int64_t w) {
+                return dtype == GR_BF16 ? piece_cost<uint16_t>(max_rows, w, dim) : piece_cost<float>(max_rows, w, dim);
+            };
+            const double c = (double)((words - 1) / vg) * cost(vg) + cost(last);
+            if (c < least * 0.999) {
+                least = c;
+                p.Vg = (int32_t)vg;
+            }
+        }
         p.G = (int64_t)p.planes * max_rows * p.Vg;
-        // a split product has at most one round of tiles (cut_product)
-        const int64_t most = (int64_t)kCUs * 256 * 256;
+        // a split product has at most kMostRounds rounds of tiles (cut_product)
+        const int64_t most = (int64_t)kMostRounds * kCUs * 256 * 256;
         const int64_t h = max_rows * p.Dp, w = (int64_t)p.Vg * p.Dp;
         p.gh = h > most ? h : (h * kMaxSplits < most ? h * kMaxSplits : most);
         p.gw = w * kMaxSplits < most ? w * kMaxSplits : most;
