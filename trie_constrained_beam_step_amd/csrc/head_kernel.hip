@@ -341,12 +341,12 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t row
 // ------------------------------------------------------------- few rows
 
 // Forward of at most 64 rows: bound by reading the table once.  A workgroup
-// takes 128 words, a wave 32 of them; the words go from memory straight to the
-// matrix cores' registers (two k steps ahead), fp32 ones split into planes on
-// the way, since each is used by one wave only.  The hidden states, which every
-// wave needs, go through LDS a k step at a time.  Nothing is packed before:
-// rows without a target are staged as zeros.
-constexpr int kFewRows = 64, kStreamWords = 128, kStreamK = 64;
+// takes 16 words a wave; the words go from memory straight to the matrix cores'
+// registers (two k steps ahead), fp32 ones split into planes on the way, since
+// each is used by one wave only.  The hidden states, which every wave needs, go
+// through LDS a k step at a time.  Nothing is packed before: rows without a
+// target are staged as zeros.
+constexpr int kFewRows = 64, kStreamK = 64;
 
 template <typename T>
 struct Raw8;  // eight elements as loaded
@@ -379,14 +379,15 @@ struct Raw8<float> {
     }
 };
 
-template <typename T, int FN>
-__global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
-    constexpr int PL = sizeof(T) == 2 ? 1 : 3, kRows = FN * 16, kItems = (kRows * 8 + 255) / 256;
+template <typename T, int FN, int Waves>
+__global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
+    constexpr int NT = Waves * 64;
+    constexpr int PL = sizeof(T) == 2 ? 1 : 3, kRows = FN * 16, kItems = (kRows * 8 + NT - 1) / NT;
     __shared__ __align__(16) uint16_t hs[2][PL][kRows][kStreamK];
-    __shared__ float sm[4][kRows], ss[4][kRows];
+    __shared__ float sm[Waves][kRows], ss[Waves][kRows];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool hwide = rows_wide((const T*)a.hidden, a.hstride), wwide = rows_wide((const T*)a.weight, a.wstride);
-    const int v0 = blockIdx.x * kStreamWords + wave * 32;
+    const int v0 = (blockIdx.x * Waves + wave) * 16;
     const int steps = tiles_of(a.D, kStreamK);
     // the width is walked in a circle from another step in every workgroup: rows
     // of the table lie a power of two apart as often as not, and workgroups in
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
     bool hok[kItems];
 #pragma unroll
     for (int q = 0; q < kItems; ++q) {
-        const int n = (q * 256 + threadIdx.x) / 8;
+        const int n = (q * NT + threadIdx.x) / 8;
         hok[q] = n < kRows && has_target(a, n);
         hrow[q] = (const T*)a.hidden + (int64_t)(hok[q] ? n : 0) * a.hstride;
     }
@@ -416,7 +417,7 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
     const auto stage_h = [&](int buf) {
 #pragma unroll
         for (int q = 0; q < kItems; ++q) {
-            const int n = (q * 256 + threadIdx.x) / 8;
+            const int n = (q * NT + threadIdx.x) / 8;
             if (n >= kRows) continue;
             bf16x8 b[PL];
             hr[q].planes(b);
@@ -425,12 +426,9 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
                 *(bf16x8*)&hs[buf][p][n][((threadIdx.x & 7) ^ along_swz<8, false>(n)) * 8] = b[p];
         }
     };
-    const T* wrow[2];
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-        wrow[f] = (const T*)a.weight + (int64_t)min(a.V - 1, v0 + f * 16 + (lane & 15)) * a.wstride;
+    const T* wrow = (const T*)a.weight + (int64_t)min(a.V - 1, v0 + (lane & 15)) * a.wstride;
     struct Words {
-        Raw8<T> r[2][2];
+        Raw8<T> r[2];
     } w0, w1;
     const auto fetch_w = [&](Words& w, int c) {
         c += turn;
@@ -438,14 +436,11 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             const int d = c * kStreamK + kk * 32 + (lane >> 4) * 8;
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                if (d < a.D) w.r[f][kk].load(wrow[f], d, a.D, wwide);
-                else w.r[f][kk].zero();
-            }
+            if (d < a.D) w.r[kk].load(wrow, d, a.D, wwide);
+            else w.r[kk].zero();
         }
     };
-    f32x4v acc[2][FN] = {};
+    f32x4v acc[FN] = {};
     const auto step = [&](int c, Words& w) {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes and reads
@@ -463,18 +458,15 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
                     const int n = j * 16 + (lane & 15);
                     b[p][j] = *(const bf16x8*)&hs[c & 1][p][n][((kk * 4 + (lane >> 4)) ^ along_swz<8, false>(n)) * 8];
                 }
+            bf16x8 x[PL];
+            w.r[kk].planes(x);
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                bf16x8 x[PL];
-                w.r[f][kk].planes(x);
+            for (int sum = PL - 1; sum >= 0; --sum)
 #pragma unroll
-                for (int sum = PL - 1; sum >= 0; --sum)
+                for (int pa = sum; pa >= 0; --pa)
 #pragma unroll
-                    for (int pa = sum; pa >= 0; --pa)
-#pragma unroll
-                        for (int j = 0; j < FN; ++j)
-                            acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[pa], b[sum - pa][j], acc[f][j], 0, 0, 0);
-            }
+                    for (int j = 0; j < FN; ++j)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[pa], b[sum - pa][j], acc[j], 0, 0, 0);
         }
         if (c + 2 < steps) fetch_w(w, c + 2);
     };
@@ -496,20 +488,16 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
         const int t = has_target(a, n) ? a.targets[n] - v0 - (lane >> 4) * 4 : -1;
         float m = kFarBelow, s = 0.0f;
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if (t == f * 16 + r) a.ws.zt[n] = acc[f][j][r] * a.scale;
-                acc[f][j][r] *= a.scale * kLog2e;
-                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) m = fmaxf(m, acc[f][j][r]);
-            }
+        for (int r = 0; r < 4; ++r) {
+            if (t == r) a.ws.zt[n] = acc[j][r] * a.scale;
+            acc[j][r] *= a.scale * kLog2e;
+            if (v0 + (lane >> 4) * 4 + r < a.V) m = fmaxf(m, acc[j][r]);
+        }
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (v0 + (lane >> 4) * 4 + f * 16 + r < a.V) s += ex2(acc[f][j][r] - m);
+        for (int r = 0; r < 4; ++r)
+            if (v0 + (lane >> 4) * 4 + r < a.V) s += ex2(acc[j][r] - m);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (lane < 16) {
@@ -520,9 +508,9 @@ __global__ __launch_bounds__(256) void head_stream_kernel(HeadArgs a) {
     __syncthreads();
     if ((int)threadIdx.x < kRows && (int)threadIdx.x < a.N) {
         const int n = threadIdx.x;
-        const float m = fmaxf(fmaxf(sm[0][n], sm[1][n]), fmaxf(sm[2][n], sm[3][n]));
-        float s = 0.0f;
-        for (int w = 0; w < 4; ++w) s += ss[w][n] * ex2(sm[w][n] - m);
+        float m = sm[0][n], s = 0.0f;
+        for (int w = 1; w < Waves; ++w) m = fmaxf(m, sm[w][n]);
+        for (int w = 0; w < Waves; ++w) s += ss[w][n] * ex2(sm[w][n] - m);
         a.ws.parts[(int64_t)blockIdx.x * a.N + n] = make_float2(m, s);
     }
 }
@@ -552,7 +540,7 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
         const int n = rn + j * 16 + (lane & 15);
         if (n >= count) continue;
         const int t = a.ws.target[n] - vp - vl;
-        const float g = a.ws.gscale[n], lse2 = a.ws.lse[n] * kLog2e;
+        const float g = a.ws.gscale[n], lse = a.ws.lse[n], lse2 = lse * kLog2e;
         const bool hit = __ballot(t >= 0 && t < Tile::WM) != 0;
 #pragma unroll
         for (int i = 0; i < Tile::FM; i += 2) {
@@ -563,7 +551,10 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int o = (i >> 1) * 32 + e + q;
-                    float p = ex2(fmaf(acc[i + (e >> 2)][j][(e & 3) + q], c, -lse2));
+                    // fp32: the difference first, or the roundings of the two
+                    // terms stay in a probability near one
+                    const float z = acc[i + (e >> 2)][j][(e & 3) + q];
+                    float p = PL == 1 ? ex2(fmaf(z, c, -lse2)) : ex2(fmaf(z, a.scale, -lse) * kLog2e);
                     if (hit && o == t) p -= 1.0f;
                     x[q] = whole || vl + o < nv ? g * p : 0.0f;
                 }
@@ -745,7 +736,6 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
     const int others = rows ? a.V : a.N;  // the length of the second product
     const int pitch = (others + 15) / 16 * 16 + 4;
     const bool hwide = rows_wide4((const T*)a.hidden, a.hstride), wwide = rows_wide4((const T*)a.weight, a.wstride);
-    const float c = a.scale * kLog2e;
 
     // Loads are from clamped places and unconditional (a branch around each would
     // leave one in flight); what does not exist is zeroed behind them.
@@ -754,7 +744,7 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
         const bool vin = v < a.V, nin = has_target(a, n);
         const T* wp = (const T*)a.weight + (int64_t)(vin ? v : 0) * a.wstride;
         const T* hp = (const T*)a.hidden + (int64_t)(nin ? n : 0) * a.hstride;
-        const float g = nin ? a.scale * a.grad_loss[n] : 0.0f, lse2 = nin ? a.lse_in[n] * kLog2e : 0.0f;
+        const float g = nin ? a.scale * a.grad_loss[n] : 0.0f, lse = nin ? a.lse_in[n] : 0.0f;
         const int t = nin ? a.targets[n] - (v - li) : -1;
         f32x4v acc = {};
         int d0 = 0;
@@ -779,7 +769,7 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int w = lk * 4 + r;
-            float p = ex2(fmaf(acc[r], c, -lse2));
+            float p = ex2(fmaf(acc[r], a.scale, -lse) * kLog2e);
             if (w == t) p -= 1.0f;
             const float x = nin && v - li + w < a.V ? g * p : 0.0f;
             if (rows) gs[li * pitch + o0 + w] = x;
@@ -906,10 +896,14 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
         a.lse = all.lse + r;
         a.grad_loss = nullptr;
         if (a.N <= kFewRows) {
-            const unsigned wgs = (unsigned)tiles_of(a.V, kStreamWords);
-            if (a.N <= 16) head_stream_kernel<T, 1><<<dim3(wgs), 256, 0, st>>>(a);
-            else if (a.N <= 32) head_stream_kernel<T, 2><<<dim3(wgs), 256, 0, st>>>(a);
-            else head_stream_kernel<T, 4><<<dim3(wgs), 256, 0, st>>>(a);
+            // more rows: more waves share the staging of the hidden states, which
+            // fp32 pays most for (64 rows of 50,257 x 768: 16 waves 46 us, 4 waves
+            // 65; one row of 151,936 x 2,048 bf16: 132 and 123 us)
+            const int waves = a.N <= 16 ? 4 : 16;
+            const unsigned wgs = (unsigned)tiles_of(a.V, waves * 16);
+            if (a.N <= 16) head_stream_kernel<T, 1, 4><<<dim3(wgs), 256, 0, st>>>(a);
+            else if (a.N <= 32) head_stream_kernel<T, 2, 16><<<dim3(wgs), 1024, 0, st>>>(a);
+            else head_stream_kernel<T, 4, 16><<<dim3(wgs), 1024, 0, st>>>(a);
             head_join_kernel<<<dim3((unsigned)a.N), 1024, 0, st>>>(a, a.N, (int)wgs, 1, false);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
