@@ -344,7 +344,14 @@ class _Table:
         self.vocab, self.dim, self.dtype, self.scale = int(vocab), int(dim), dtype, float(scale)
         self._torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self._gr_dtype = _lib.GR_BF16 if dtype == "bf16" else _lib.GR_F32
+        self._torch = torch
         self._h = None
+
+    def _made(self, handle):
+        """The handle of an init call, and the device it was made on."""
+        self._h = handle
+        self._index = self._torch.cuda.current_device()
+        self.device = self._torch.device("cuda", self._index)
 
     @property
     def handle(self):
@@ -353,16 +360,14 @@ class _Table:
         return self._h
 
     def _tensor(self, t, name, dtype):
-        import torch
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        if not isinstance(t, self._torch.Tensor) or not t.is_cuda or t.dtype != dtype:
             raise TypeError(f"{name} must be a cuda {dtype} tensor")
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the {type(self).__name__.lower()} on {self.device}")
-        return t
 
     def _flat(self, t, name, dtype, n=None):
         """A contiguous tensor (of n elements): its address."""
-        t = self._tensor(t, name, dtype)
+        self._tensor(t, name, dtype)
         if not t.is_contiguous() or (n is not None and t.numel() != n):
             raise ValueError(f"{name} must be contiguous" + (f" with {n} elements" if n is not None else ""))
         return t.data_ptr()
@@ -370,43 +375,45 @@ class _Table:
     def _rows(self, t, name, n):
         """n rows of `dim` elements, [n, dim] with any row stride or contiguous
         [..., dim]: their address and row stride."""
-        t = self._tensor(t, name, self._torch_dtype)
-        if t.dim() < 2 or t.shape[-1] != self.dim or t.numel() != n * self.dim:
-            raise ValueError(f"{name} must hold {n} rows of {self.dim}, not {tuple(t.shape)}")
+        self._tensor(t, name, self._torch_dtype)
+        dim = self.dim
+        if t.dim() < 2 or t.shape[-1] != dim or t.numel() != n * dim:
+            raise ValueError(f"{name} must hold {n} rows of {dim}, not {tuple(t.shape)}")
         if t.is_contiguous():
-            return t.data_ptr(), self.dim
-        if t.dim() != 2 or (self.dim > 1 and t.stride(1) != 1) or t.stride(0) < self.dim:
+            return t.data_ptr(), dim
+        if t.dim() != 2 or (dim > 1 and t.stride(1) != 1) or t.stride(0) < dim:
             raise ValueError(f"{name} must be contiguous, or [n, dim] with rows of consecutive elements that do not overlap")
         return t.data_ptr(), t.stride(0)
 
     def _stream(self, stream):
-        """The torch stream to enqueue on (default: the current one of the
-        handle's device)."""
-        import torch
-        if stream is None:
-            return torch.cuda.current_stream(self.device)
+        """The torch stream a caller gave, checked; an address becomes a stream."""
         if hasattr(stream, "cuda_stream"):
             if stream.device != self.device:
                 raise ValueError(f"the stream is on {stream.device}, the {type(self).__name__.lower()} on {self.device}")
             return stream
-        return torch.cuda.ExternalStream(int(stream), device=self.device)
+        return self._torch.cuda.ExternalStream(int(stream), device=self.device)
+
+    def _stream_ptr(self, stream):
+        """The address of the stream to enqueue on (default: torch's current one
+        of the handle's device)."""
+        if stream is None:
+            return self._torch.cuda.current_stream(self._index).cuda_stream
+        return self._stream(stream).cuda_stream
 
     def _empty(self, shape, dtype, stream):
         """A new output, owned by the stream that writes it."""
-        import torch
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self._stream(stream)):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
+        with self._torch.cuda.stream(self._stream(stream)):
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
 
     def _used(self, stream, *tensors):
         """Tensors that work on a `stream` given by the caller reads or writes:
         their memory is not reused before that work is done."""
-        if stream is not None:
-            s = self._stream(stream)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(s)
+        s = self._stream(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
 
     def close(self):
         if getattr(self, "_h", None) is not None:
@@ -427,48 +434,47 @@ class Embedding(_Table):
     max_tokens: the most tokens of one call."""
 
     def __init__(self, vocab: int, dim: int, max_tokens: int, *, dtype: str = "f32", scale: float = 1.0, stream=None):
-        import torch
         self._setup(vocab, dim, dtype, scale)
         self.max_tokens = int(max_tokens)
-        self._free = lib().gr_embed_free
+        L = lib()
+        self._free, self._lookup, self._backward = L.gr_embed_free, L.gr_embed_lookup, L.gr_embed_backward
         cfg = EmbedConfig(vocab=self.vocab, dim=self.dim, max_tokens=self.max_tokens, dtype=self._gr_dtype,
                           scale=self.scale)
         h = C.c_void_p()
         _check(lib().gr_embed_init(C.byref(cfg), None if stream is None else _stream_ptr(stream), C.byref(h)))
-        self._h = h
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._made(h)
 
     def lookup(self, tokens, weight, out=None, stream=None):
         """scale * weight[tokens]: tokens a contiguous cuda int32 tensor of any
         shape, weight [vocab, dim]; returns [*tokens.shape, dim] (`out`, if given)."""
-        import torch
+        torch = self._torch
         pt = self._flat(tokens, "tokens", torch.int32)
         n = tokens.numel()
         pw, sw = self._rows(weight, "weight", self.vocab)
-        s = self._stream(stream)
         if out is None:
             out = self._empty((*tokens.shape, self.dim), self._torch_dtype, stream)
         po, so = self._rows(out, "out", n)
-        _check(lib().gr_embed_lookup(self.handle, pt, n, pw, sw, po, so, s.cuda_stream))
-        self._used(stream, tokens, weight)
+        _check(self._lookup(self.handle, pt, n, pw, sw, po, so, self._stream_ptr(stream)))
+        if stream is not None:
+            self._used(stream, tokens, weight)
         return out
 
     def backward(self, tokens, grad, grad_weight=None, accumulate: bool = False, stream=None):
         """The table's gradient [vocab, dim] from grad [*tokens.shape, dim], the
         gradient of lookup's result.  grad_weight: written whole, or added to
         with accumulate=True; a new tensor if None."""
-        import torch
+        torch = self._torch
         pt = self._flat(tokens, "tokens", torch.int32)
         n = tokens.numel()
         pg, sg = self._rows(grad, "grad", n)
-        s = self._stream(stream)
         if grad_weight is None:
             if accumulate:
                 raise ValueError("accumulate needs the grad_weight to add to")
             grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, stream)
         pw, sw = self._rows(grad_weight, "grad_weight", self.vocab)
-        _check(lib().gr_embed_backward(self.handle, pt, n, pg, sg, pw, sw, 1 if accumulate else 0, s.cuda_stream))
-        self._used(stream, tokens, grad, grad_weight)
+        _check(self._backward(self.handle, pt, n, pg, sg, pw, sw, 1 if accumulate else 0, self._stream_ptr(stream)))
+        if stream is not None:
+            self._used(stream, tokens, grad, grad_weight)
         return grad_weight
 
 
@@ -480,30 +486,30 @@ class Head(_Table):
 
     def __init__(self, vocab: int, dim: int, max_rows: int, *, dtype: str = "f32", scale: float = 1.0,
                  backward: bool = True, stream=None):
-        import torch
         self._setup(vocab, dim, dtype, scale)
         self.max_rows = int(max_rows)
-        self._free = lib().gr_head_free
+        L = lib()
+        self._free, self._loss, self._backward = L.gr_head_free, L.gr_head_loss, L.gr_head_backward
         cfg = HeadConfig(vocab=self.vocab, dim=self.dim, max_rows=self.max_rows, dtype=self._gr_dtype,
                          scale=self.scale, score_only=0 if backward else 1)
         h = C.c_void_p()
         _check(lib().gr_head_init(C.byref(cfg), None if stream is None else _stream_ptr(stream), C.byref(h)))
-        self._h = h
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._made(h)
 
     def loss(self, hidden, weight, targets, stream=None):
         """(loss, lse), float32 of targets' shape: -log p of each row's target
         and the row's log-softmax normaliser.  hidden [*targets.shape, dim],
         weight [vocab, dim], targets a contiguous cuda int32 tensor."""
-        import torch
+        torch = self._torch
         pt = self._flat(targets, "targets", torch.int32)
         n = targets.numel()
         ph, sh = self._rows(hidden, "hidden", n)
         pw, sw = self._rows(weight, "weight", self.vocab)
-        s = self._stream(stream)
-        loss, lse = (self._empty(targets.shape, torch.float32, stream) for _ in range(2))
-        _check(lib().gr_head_loss(self.handle, ph, sh, pw, sw, pt, n, loss.data_ptr(), lse.data_ptr(), s.cuda_stream))
-        self._used(stream, hidden, weight, targets)
+        loss = self._empty(targets.shape, torch.float32, stream)
+        lse = self._empty(targets.shape, torch.float32, stream)
+        _check(self._loss(self.handle, ph, sh, pw, sw, pt, n, loss.data_ptr(), lse.data_ptr(), self._stream_ptr(stream)))
+        if stream is not None:
+            self._used(stream, hidden, weight, targets)
         return loss, lse
 
     def backward(self, hidden, weight, targets, lse, grad_loss, grad_hidden=None, grad_weight=None,
@@ -512,7 +518,7 @@ class Head(_Table):
         grad_loss (float32, targets' shape) and loss()'s lse.  grad_hidden,
         grad_weight: tensors to write (new ones if None); accumulate=True adds
         to grad_weight.  need: which of the two to compute; the other is None."""
-        import torch
+        torch = self._torch
         pt = self._flat(targets, "targets", torch.int32)
         n = targets.numel()
         ph, sh = self._rows(hidden, "hidden", n)
@@ -522,7 +528,6 @@ class Head(_Table):
         need = set(need)
         if not need or not need <= {"hidden", "weight"}:
             raise ValueError("need names 'hidden', 'weight' or both")
-        s = self._stream(stream)
         pgh = pgw = None
         sgh = sgw = 0
         if "hidden" not in need:
@@ -539,9 +544,10 @@ class Head(_Table):
                     raise ValueError("accumulate needs the grad_weight to add to")
                 grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, stream)
             pgw, sgw = self._rows(grad_weight, "grad_weight", self.vocab)
-        _check(lib().gr_head_backward(self.handle, ph, sh, pw, sw, pt, n, pl, pg, pgh, sgh, pgw, sgw,
-                                      1 if accumulate else 0, s.cuda_stream))
-        self._used(stream, hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
+        _check(self._backward(self.handle, ph, sh, pw, sw, pt, n, pl, pg, pgh, sgh, pgw, sgw,
+                                      1 if accumulate else 0, self._stream_ptr(stream)))
+        if stream is not None:
+            self._used(stream, hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
         return grad_hidden, grad_weight
 
 

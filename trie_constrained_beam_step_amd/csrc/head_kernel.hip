@@ -233,11 +233,14 @@ __device__ __forceinline__ Operand grad_operand(const HeadArgs& a, int64_t rows_
 
 // --------------------------------------------------- logits and their uses
 
+constexpr int kPartWords = 64;  // of a part at least: sizes the parts' buffer
+
 // A wave's accumulators (gemm_tile.h): fragments 2i and 2i+1 of a lane hold the
 // eight words rm + 32*i + (lane/16)*8 + 0..7 of hidden state rn + 16*j + lane%16.
 
 template <typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
+    static_assert(Tile::WM >= kPartWords, "a part for each wave's words");
     __shared__ __align__(1024) char lds[2 * Tile::Stage];
     const int count = *a.ws.count;
     int im, in;
@@ -346,7 +349,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t row
 // each is used by one wave only.  The hidden states, which every wave needs, go
 // through LDS a k step at a time.  Nothing is packed before: rows without a
 // target are staged as zeros.
-constexpr int kFewRows = 64, kStreamK = 64;
+constexpr int kFewRows = 64;
 
 template <typename T>
 struct Raw8;  // eight elements as loaded
@@ -379,16 +382,18 @@ struct Raw8<float> {
     }
 };
 
-template <typename T, int FN, int Waves>
+template <typename T, int FN, int Waves, int StepK>
 __global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
+    static_assert(Waves * 16 >= kPartWords, "a part for each workgroup");
     constexpr int NT = Waves * 64;
-    constexpr int PL = sizeof(T) == 2 ? 1 : 3, kRows = FN * 16, kItems = (kRows * 8 + NT - 1) / NT;
-    __shared__ __align__(16) uint16_t hs[2][PL][kRows][kStreamK];
+    constexpr int PL = sizeof(T) == 2 ? 1 : 3, kRows = FN * 16, kChunks = StepK / 8;
+    constexpr int kItems = (kRows * kChunks + NT - 1) / NT, kParts32 = StepK / 32;
+    __shared__ __align__(16) uint16_t hs[2][PL][kRows][StepK];
     __shared__ float sm[Waves][kRows], ss[Waves][kRows];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool hwide = rows_wide((const T*)a.hidden, a.hstride), wwide = rows_wide((const T*)a.weight, a.wstride);
     const int v0 = (blockIdx.x * Waves + wave) * 16;
-    const int steps = tiles_of(a.D, kStreamK);
+    const int steps = tiles_of(a.D, StepK);
     // the width is walked in a circle from another step in every workgroup: rows
     // of the table lie a power of two apart as often as not, and workgroups in
     // step with one another would all ask the same memory channels
@@ -399,7 +404,7 @@ __global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
     bool hok[kItems];
 #pragma unroll
     for (int q = 0; q < kItems; ++q) {
-        const int n = (q * NT + threadIdx.x) / 8;
+        const int n = (q * NT + threadIdx.x) / kChunks;
         hok[q] = n < kRows && has_target(a, n);
         hrow[q] = (const T*)a.hidden + (int64_t)(hok[q] ? n : 0) * a.hstride;
     }
@@ -409,7 +414,7 @@ __global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
         c -= c >= steps ? steps : 0;
 #pragma unroll
         for (int q = 0; q < kItems; ++q) {
-            const int d = c * kStreamK + (threadIdx.x & 7) * 8;
+            const int d = c * StepK + (threadIdx.x % kChunks) * 8;
             if (hok[q] && d < a.D) hr[q].load(hrow[q], d, a.D, hwide);
             else hr[q].zero();
         }
@@ -417,25 +422,25 @@ __global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
     const auto stage_h = [&](int buf) {
 #pragma unroll
         for (int q = 0; q < kItems; ++q) {
-            const int n = (q * NT + threadIdx.x) / 8;
+            const int n = (q * NT + threadIdx.x) / kChunks;
             if (n >= kRows) continue;
             bf16x8 b[PL];
             hr[q].planes(b);
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-                *(bf16x8*)&hs[buf][p][n][((threadIdx.x & 7) ^ along_swz<8, false>(n)) * 8] = b[p];
+                *(bf16x8*)&hs[buf][p][n][((threadIdx.x % kChunks) ^ along_swz<8, false>(n)) * 8] = b[p];
         }
     };
     const T* wrow = (const T*)a.weight + (int64_t)min(a.V - 1, v0 + (lane & 15)) * a.wstride;
     struct Words {
-        Raw8<T> r[2];
+        Raw8<T> r[kParts32];
     } w0, w1;
     const auto fetch_w = [&](Words& w, int c) {
         c += turn;
         c -= c >= steps ? steps : 0;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const int d = c * kStreamK + kk * 32 + (lane >> 4) * 8;
+        for (int kk = 0; kk < kParts32; ++kk) {
+            const int d = c * StepK + kk * 32 + (lane >> 4) * 8;
             if (d < a.D) w.r[kk].load(wrow, d, a.D, wwide);
             else w.r[kk].zero();
         }
@@ -449,7 +454,7 @@ __global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
         if (c + 1 < steps) stage_h((c + 1) & 1);
         if (c + 2 < steps) fetch_h(c + 2);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+        for (int kk = 0; kk < kParts32; ++kk) {
             bf16x8 b[PL][FN];
 #pragma unroll
             for (int p = 0; p < PL; ++p)
@@ -899,11 +904,12 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
             // more rows: more waves share the staging of the hidden states, which
             // fp32 pays most for (64 rows of 50,257 x 768: 16 waves 46 us, 4 waves
             // 65; one row of 151,936 x 2,048 bf16: 132 and 123 us)
+            constexpr int kWide = 256 / sizeof(T);  // 256 bytes of a row a step: 116 us, 128 bytes 122, 512 bytes 120
             const int waves = a.N <= 16 ? 4 : 16;
             const unsigned wgs = (unsigned)tiles_of(a.V, waves * 16);
-            if (a.N <= 16) head_stream_kernel<T, 1, 4><<<dim3(wgs), 256, 0, st>>>(a);
-            else if (a.N <= 32) head_stream_kernel<T, 2, 16><<<dim3(wgs), 1024, 0, st>>>(a);
-            else head_stream_kernel<T, 4, 16><<<dim3(wgs), 1024, 0, st>>>(a);
+            if (a.N <= 16) head_stream_kernel<T, 1, 4, kWide><<<dim3(wgs), 256, 0, st>>>(a);
+            else if (a.N <= 32) head_stream_kernel<T, 2, 16, 64><<<dim3(wgs), 1024, 0, st>>>(a);
+            else head_stream_kernel<T, 4, 16, 64><<<dim3(wgs), 1024, 0, st>>>(a);
             head_join_kernel<<<dim3((unsigned)a.N), 1024, 0, st>>>(a, a.N, (int)wgs, 1, false);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
@@ -1026,7 +1032,7 @@ HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool
     const int64_t vw = kTableElems / p.planes / p.Dp / kWordTile * kWordTile;
     p.Vw = (int32_t)(vw < kWordTile ? kWordTile : (vw < words ? vw : words));
     p.W = (int64_t)p.planes * p.Vw * p.Dp;
-    p.parts = (vocab + 63) / 64 * (int64_t)p.part_rows;  // the narrowest wave: 64 words
+    p.parts = (vocab + kPartWords - 1) / kPartWords * (int64_t)p.part_rows;
     if (backward) {
         const int64_t vg = kPieceElems / p.planes / max_rows / kWordTile * kWordTile;
         const int64_t most_words = vg < kWordTile ? kWordTile : (vg < words ? vg : words);
