@@ -9,12 +9,20 @@
 // (ds_read_b64_tr_b16: 16 lanes read four k rows of 16 elements, and lane i
 // gets the four of column i).  So one table serves W, W^T, H, H^T, G and G^T.
 //
-// Planes.  An fp32 operand is held as three bf16 planes, x = x0 + x1 + x2, each
-// the bf16 nearest to what the ones before it leave: 8 significant bits a
-// plane, so the sum is x itself.  A product takes the six pairs of planes whose
-// index sum is at most two; the three left out are below 2^-23 |a b|.  Six
-// bf16 products run 2.8 times as fast as one fp32 product on these cores
-// (dense peaks 2.5 PFLOP/s against 157 TFLOP/s, over six).
+// Planes.  An fp32 operand is held in planes of 16 bits, x = x0 + x1 (+ x2), each
+// the nearest to what the ones before it leave; a product takes the pairs of
+// planes whose index sum is below their number, and sums them in fp32.  fp32
+// matrix instructions run at 157 TFLOP/s, 16-bit ones at 2.5 PFLOP/s.
+//   three bf16 planes, six pairs: 8 significant bits a plane, so the sum is x
+//     itself, over the whole range of fp32; the pairs left out are below 2^-23
+//     |a b|.
+//   two fp16 planes, three pairs (Half): 11 bits a plane leave x0 + x1 within
+//     2^-22 of x, if x is between 2^-14 and 2^16: for operands whose rows can
+//     be scaled by a power of two that divides out of the product again (the
+//     logits' both; 2^15 is put on a row's largest element, and elements down
+//     to 2^-17 of it keep their 22 bits, smaller ones are off by 2^-40 of the
+//     largest).  With the pair left out a product is off by 3 * 2^-22 |a b| at
+//     most, a few roundings of an fp32 sum.
 //
 // Bounds.  Every load goes through a buffer descriptor that ends with the
 // operand, so rows behind its last one read as zero.
@@ -66,9 +74,18 @@ __device__ __forceinline__ int frag_row(int t, int i) {
     return Perm ? (t >> 1) * 32 + (i >> 2) * 8 + (t & 1) * 4 + (i & 3) : t * 16 + i;
 }
 
-// BM x BN tile, waves of WM x WN, BK deep (32 or 64), PL planes.
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int PL_, bool AAcross, bool BAcross>
+// One step of the matrix cores on 16 x 16 x 32 elements of either 16-bit type.
+template <bool Half>
+__device__ __forceinline__ f32x4v mfma16(bf16x8 a, bf16x8 b, f32x4v c) {
+    typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+    if (Half) return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// BM x BN tile, waves of WM x WN, BK deep (32 or 64), PL planes (Half: of fp16).
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int PL_, bool AAcross, bool BAcross, bool Half_ = false>
 struct GemmTile {
+    static constexpr bool Half = Half_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, PL = PL_;
     static constexpr int NT = (BM / WM) * (BN / WN) * 64;
     static constexpr int FM = WM / 16, FN = WN / 16;
@@ -183,8 +200,7 @@ struct GemmTile {
                 for (int pa = sum; pa >= 0; --pa)
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
-                        acc[s % FM][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[s % (kAhead + 1)][pa], b[(s / FM) & 1][sum - pa][j],
-                                                                                acc[s % FM][j], 0, 0, 0);
+                        acc[s % FM][j] = mfma16<Half>(a[s % (kAhead + 1)][pa], b[(s / FM) & 1][sum - pa][j], acc[s % FM][j]);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -285,8 +301,7 @@ struct GemmTile {
                         for (int q = 0; q < FM; ++q)
 #pragma unroll
                             for (int j = 0; j < FN; ++j)
-                                acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[kk][pa][q], b[kk][sum - pa][j], acc[q][j],
-                                                                                    0, 0, 0);
+                                acc[q][j] = mfma16<Half>(a[kk][pa][q], b[kk][sum - pa][j], acc[q][j]);
             __builtin_amdgcn_s_setprio(0);
             stage_barrier(!second);
         }

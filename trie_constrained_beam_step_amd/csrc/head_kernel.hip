@@ -105,6 +105,39 @@ __device__ __forceinline__ void pack_row(const float* src, int D, int Dp, bool w
     }
 }
 
+// Row `src` scaled by a power of two into two fp16 planes (gemm_tile.h), by one
+// wave; returns what divides the scale out again.
+__device__ __forceinline__ float pack_row_half(const float* src, int D, int Dp, bool wide, uint16_t* dst, int64_t plane, int lane) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    float most = 0.0f;
+    for (int d = lane * 8; d < Dp; d += 512) {
+        float x[8];
+        load8(src, d, D, wide, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
+    }
+    most = wave_max(most);
+    const int exponent = (int)((__float_as_uint(most) >> 23) & 255) - 127;
+    const int up = most == 0.0f ? 0 : min(126, 14 - exponent);  // 2^14 <= most * 2^up < 2^15
+    const float scale = __uint_as_float((uint32_t)(127 + up) << 23);
+    for (int d = lane * 8; d < Dp; d += 512) {
+        float x[8];
+        load8(src, d, D, wide, x);
+        u32x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float y0 = x[2 * e] * scale, y1 = x[2 * e + 1] * scale;
+            const f16x2 h = {(_Float16)y0, (_Float16)y1};
+            const f16x2 l = {(_Float16)(y0 - (float)h[0]), (_Float16)(y1 - (float)h[1])};
+            hi[e] = __builtin_bit_cast(uint32_t, h);
+            lo[e] = __builtin_bit_cast(uint32_t, l);
+        }
+        *(u32x4*)(dst + d) = hi;
+        *(u32x4*)(dst + plane + d) = lo;
+    }
+    return __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
 // Rows from `p` on, `stride` apart, all start on 16 bytes.
 template <typename T>
 __device__ __forceinline__ bool rows_wide(const T* p, int64_t stride) {
@@ -112,12 +145,15 @@ __device__ __forceinline__ bool rows_wide(const T* p, int64_t stride) {
 }
 
 constexpr int kPackRows = 16;  // rows of a workgroup
+// what a packing kernel writes: planes as they are (bf16: one, fp32: three, for
+// the gradients' products), scaled halves (fp32, for the logits)
+constexpr int kPackPlanes = 1, kPackHalves = 2;
 
 // The rows that have a target, packed in order.  Each workgroup counts the
 // targets before its own rows by itself (the targets of 2^16 rows are 256 KB
 // of L2 reads; a scan kernel before this one would cost a launch).
 template <typename T>
-__global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows_cap, int rows_per_wg, bool zero_rows) {
+__global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows_cap, int rows_per_wg, int what, bool zero_rows) {
     __shared__ int wsum[4], base;
     const int r0 = blockIdx.x * rows_per_wg;
     int c = 0;
@@ -160,9 +196,15 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
         int k = 0;
         for (uint64_t rest = m; rest; rest &= rest - 1, ++k) {
             if ((k & 3) != wave) continue;
-            const int row = r1 + __builtin_ctzll(rest);
-            pack_row((const T*)a.hidden + (int64_t)row * a.hstride, a.D, a.plan.Dp, wide,
-                     a.ws.H + (int64_t)(before + k) * a.plan.Dp, rows_cap * a.plan.Dp, lane, 64);
+            const T* src = (const T*)a.hidden + (int64_t)(r1 + __builtin_ctzll(rest)) * a.hstride;
+            const int64_t at = (int64_t)(before + k) * a.plan.Dp, plane = rows_cap * a.plan.Dp;
+            if (what & kPackPlanes) pack_row(src, a.D, a.plan.Dp, wide, a.ws.H + at, plane, lane, 64);
+            if constexpr (sizeof(T) == 4) {
+                if (what & kPackHalves) {
+                    const float f = pack_row_half(src, a.D, a.plan.Dp, wide, a.ws.Hh + at, plane, lane);
+                    if (lane == 0) a.ws.hdown[before + k] = f;
+                }
+            }
         }
         if (zero_rows) {  // rows of grad_hidden without a target
             uint64_t none = ~m;
@@ -178,13 +220,21 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
     if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) *a.ws.count = before;
 }
 
-// Words [v0, v0 + nv) of the table in planes.
+// Words [v0, v0 + nv) of the table.
 template <typename T>
-__global__ __launch_bounds__(256) void pack_words_kernel(HeadArgs a, int v0, int nv) {
-    const int v = blockIdx.x * 4 + (threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void pack_words_kernel(HeadArgs a, int v0, int nv, int what) {
+    const int v = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (v >= nv) return;
-    pack_row((const T*)a.weight + (int64_t)(v0 + v) * a.wstride, a.D, a.plan.Dp, rows_wide((const T*)a.weight, a.wstride),
-             a.ws.W + (int64_t)v * a.plan.Dp, (int64_t)a.plan.Vw * a.plan.Dp, threadIdx.x & 63, 64);
+    const T* src = (const T*)a.weight + (int64_t)(v0 + v) * a.wstride;
+    const bool wide = rows_wide((const T*)a.weight, a.wstride);
+    const int64_t at = (int64_t)v * a.plan.Dp, plane = (int64_t)a.plan.Vw * a.plan.Dp;
+    if (what & kPackPlanes) pack_row(src, a.D, a.plan.Dp, wide, a.ws.W + at, plane, lane, 64);
+    if constexpr (sizeof(T) == 4) {
+        if (what & kPackHalves) {
+            const float f = pack_row_half(src, a.D, a.plan.Dp, wide, a.ws.Wh + at, plane, lane);
+            if (lane == 0) a.ws.wdown[v] = f;
+        }
+    }
 }
 
 // ----------------------------------------------------------- tile order
@@ -224,6 +274,24 @@ struct TileFor<float, AAcross, BAcross, false> {
     typedef GemmTile<128, 128, 64, 64, 32, 3, AAcross, BAcross> type;
 };
 
+// The logits' product: halves where the elements are fp32.
+template <typename T, bool Large>
+struct LogitTile {
+    typedef typename TileFor<T, false, false, Large>::type type;
+};
+template <>
+struct LogitTile<float, true> {
+    typedef GemmTile<256, 256, 128, 64, 32, 2, false, false, true> type;
+};
+template <>
+struct LogitTile<float, false> {
+    typedef GemmTile<128, 128, 64, 64, 32, 2, false, false, true> type;
+};
+
+template <typename Tile>
+__device__ __forceinline__ Operand logit_hidden(const HeadArgs& a, int64_t rows_cap, int count) {
+    return Operand{Tile::Half ? a.ws.Hh : a.ws.H, a.plan.Dp, rows_cap * a.plan.Dp, (int64_t)count * a.plan.Dp};
+}
 __device__ __forceinline__ Operand hidden_operand(const HeadArgs& a, int64_t rows_cap, int count) {
     return Operand{a.ws.H, a.plan.Dp, rows_cap * a.plan.Dp, (int64_t)count * a.plan.Dp};
 }
@@ -234,6 +302,19 @@ __device__ __forceinline__ Operand grad_operand(const HeadArgs& a, int64_t rows_
 // --------------------------------------------------- logits and their uses
 
 constexpr int kPartWords = 64;  // of a part at least: sizes the parts' buffer
+
+// Halves: the words' scales, divided out of a wave's accumulators (rows rm on of
+// the piece); the hidden states' are left to their factors.
+template <typename Tile>
+__device__ __forceinline__ void unscale_words(const HeadArgs& a, int rm, f32x4v (&acc)[Tile::FM][Tile::FN]) {
+    if (!Tile::Half) return;
+#pragma unroll
+    for (int i = 0; i < Tile::FM; ++i) {
+        const f32x4v w = *(const f32x4v*)(a.ws.wdown + rm + (i >> 1) * 32 + ((threadIdx.x & 63) >> 4) * 8 + (i & 1) * 4);
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j) acc[i][j] *= w;
+    }
+}
 
 // A wave's accumulators (gemm_tile.h): fragments 2i and 2i+1 of a lane hold the
 // eight words rm + 32*i + (lane/16)*8 + 0..7 of hidden state rn + 16*j + lane%16.
@@ -248,24 +329,26 @@ __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operan
     const int m0 = im * Tile::BM, n0 = in * Tile::BN;
     if (n0 >= count) return;
     f32x4v acc[Tile::FM][Tile::FN] = {};
-    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, lds, acc);
+    Tile::run(W, m0, logit_hidden<Tile>(a, rows_cap, count), n0, 0, a.D, lds, acc);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
     if (rm >= nv) return;
     const int vl = vp + rm + (lane >> 4) * 8;  // word of acc[0][j][0]
     const int part = (vp + rm) / Tile::WM;
-    const float c = a.scale * kLog2e;
+    unscale_words<Tile>(a, rm, acc);
+    float down[Tile::FN];  // the row's factor: the logits' scale, and its own
 #pragma unroll
     for (int j = 0; j < Tile::FN; ++j) {
         const int n = rn + j * 16 + (lane & 15);
+        down[j] = Tile::Half && n < count ? a.scale * a.ws.hdown[n] : a.scale;
         const int t = n < count ? a.ws.target[n] - vl : -1;
         if (__ballot(t >= 0 && t < Tile::WM) == 0) continue;
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if ((i >> 1) * 32 + (i & 1) * 4 + r == t) a.ws.zt[n] = acc[i][j][r] * a.scale;
+                if ((i >> 1) * 32 + (i & 1) * 4 + r == t) a.ws.zt[n] = acc[i][j][r] * down[j];
     }
     // from here on in units of log 2: y = z log2 e
 #pragma unroll
@@ -273,7 +356,7 @@ __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operan
 #pragma unroll
         for (int j = 0; j < Tile::FN; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] *= c;
+            for (int r = 0; r < 4; ++r) acc[i][j][r] *= down[j] * kLog2e;
     if (vp + rm + Tile::WM > a.V) {  // words behind the table take no part
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i)
@@ -525,21 +608,21 @@ __global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
 template <typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
     __shared__ __align__(1024) char lds[2 * Tile::Stage];
-    constexpr int PL = Tile::PL;
+    constexpr int PL = Tile::Half ? 3 : Tile::PL;  // of G
     const int count = *a.ws.count;
     int im, in;
     tile_of(blockIdx.x, tiles_of(nv, Tile::BM), tiles_of(a.N, Tile::BN), im, in);
     const int m0 = im * Tile::BM, n0 = in * Tile::BN;
     if (n0 >= count) return;
     f32x4v acc[Tile::FM][Tile::FN] = {};
-    Tile::run(W, m0, hidden_operand(a, rows_cap, count), n0, 0, a.D, lds, acc);
+    Tile::run(W, m0, logit_hidden<Tile>(a, rows_cap, count), n0, 0, a.D, lds, acc);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
     const int vl = rm + (lane >> 4) * 8;
     const int64_t plane = rows_cap * a.plan.Vg;
-    const float c = a.scale * kLog2e;
     const bool whole = rm + Tile::WM <= nv;
+    unscale_words<Tile>(a, rm, acc);
 #pragma unroll
     for (int j = 0; j < Tile::FN; ++j) {
         const int n = rn + j * 16 + (lane & 15);
@@ -547,6 +630,7 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
         const int t = a.ws.target[n] - vp - vl;
         const float g = a.ws.gscale[n], lse = a.ws.lse[n], lse2 = lse * kLog2e;
         const bool hit = __ballot(t >= 0 && t < Tile::WM) != 0;
+        const float down = Tile::Half ? a.scale * a.ws.hdown[n] : a.scale, c = down * kLog2e;
 #pragma unroll
         for (int i = 0; i < Tile::FM; i += 2) {
             u32x4 out[PL];
@@ -559,7 +643,7 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
                     // fp32: the difference first, or the roundings of the two
                     // terms stay in a probability near one
                     const float z = acc[i + (e >> 2)][j][(e & 3) + q];
-                    float p = PL == 1 ? ex2(fmaf(z, c, -lse2)) : ex2(fmaf(z, a.scale, -lse) * kLog2e);
+                    float p = PL == 1 ? ex2(fmaf(z, c, -lse2)) : ex2(fmaf(z, down, -lse) * kLog2e);
                     if (hit && o == t) p -= 1.0f;
                     x[q] = whole || vl + o < nv ? g * p : 0.0f;
                 }
@@ -863,23 +947,32 @@ bool reads_in_place(const void* p, int64_t stride, int D, int dtype) {
 }
 
 template <typename T>
-hipError_t pack_rows(const HeadArgs& a, int64_t cap, bool zero_rows, hipStream_t st) {
+hipError_t pack_rows(const HeadArgs& a, int64_t cap, int what, bool zero_rows, hipStream_t st) {
     int per = kPackRows;
     while (tiles_of(a.N, per) > 4096) per *= 2;  // the count before a workgroup's rows is quadratic in their number
-    pack_rows_kernel<T><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per, zero_rows);
+    pack_rows_kernel<T><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per, what, zero_rows);
     return hipGetLastError();
 }
 
-// The operand of words [v, v + nv), packed first where it cannot be read in place.
+// Words [v, v + nv) as the operand of the logits and of grad_hidden, packed first
+// where they cannot be read in place.
+struct Words {
+    Operand logits, planes;
+};
+
 template <typename T>
-Operand words_operand(const HeadArgs& a, int v, int nv, int dtype, hipStream_t st) {
+Words words_operands(const HeadArgs& a, int v, int nv, bool planes, int dtype, hipStream_t st) {
     const int Dp = a.plan.Dp;
     if (reads_in_place(a.weight, a.wstride, a.D, dtype)) {
         const uint16_t* p = (const uint16_t*)a.weight + (int64_t)v * a.wstride;
-        return Operand{p, a.wstride, 0, (int64_t)(nv - 1) * a.wstride + a.D};
+        const Operand w{p, a.wstride, 0, (int64_t)(nv - 1) * a.wstride + a.D};
+        return Words{w, w};
     }
-    pack_words_kernel<T><<<dim3((unsigned)tiles_of(nv, 4)), 256, 0, st>>>(a, v, nv);
-    return Operand{a.ws.W, Dp, (int64_t)a.plan.Vw * Dp, (int64_t)nv * Dp};
+    const int64_t plane = (int64_t)a.plan.Vw * Dp;
+    const bool half = sizeof(T) == 4;
+    const int what = half ? kPackHalves + (planes ? kPackPlanes : 0) : kPackPlanes;
+    pack_words_kernel<T><<<dim3((unsigned)tiles_of(nv, 4)), 256, 0, st>>>(a, v, nv, what);
+    return Words{Operand{half ? a.ws.Wh : a.ws.W, Dp, plane, (int64_t)nv * Dp}, Operand{a.ws.W, Dp, plane, (int64_t)nv * Dp}};
 }
 
 template <typename Tile>
@@ -889,8 +982,8 @@ void run_parts(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, 
 
 template <typename T>
 hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
-    typedef typename TileFor<T, false, false, true>::type Large;
-    typedef typename TileFor<T, false, false, false>::type Small;
+    typedef typename LogitTile<T, true>::type Large;
+    typedef typename LogitTile<T, false>::type Small;
     const int64_t cap = all.plan.part_rows;
     for (int64_t r = 0; r < all.N; r += cap) {
         HeadArgs a = all;
@@ -915,13 +1008,13 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
             if (e != hipSuccess) return e;
             continue;
         }
-        hipError_t e = pack_rows<T>(a, cap, false, st);
+        hipError_t e = pack_rows<T>(a, cap, dtype == GR_BF16 ? kPackPlanes : kPackHalves, false, st);
         if (e != hipSuccess) return e;
         const bool large = cut_product<Large, Small>(a.V, a.N, a.D, false, kLogitEnds).large;
         const int step = reads_in_place(a.weight, a.wstride, a.D, dtype) ? a.V : a.plan.Vw;
         for (int v = 0; v < a.V; v += step) {
             const int nv = a.V - v < step ? a.V - v : step;
-            const Operand W = words_operand<T>(a, v, nv, dtype, st);
+            const Operand W = words_operands<T>(a, v, nv, false, dtype, st).logits;
             if (large) run_parts<Large>(a, W, cap, v, nv, st);
             else run_parts<Small>(a, W, cap, v, nv, st);
         }
@@ -967,8 +1060,8 @@ bool small_backward(const HeadArgs& a, int dtype) {
 // Cost of the three products of a piece of `words` words.
 template <typename T>
 double piece_cost(int64_t rows, int64_t words, int64_t dim) {
-    typedef typename TileFor<T, false, false, true>::type ZLarge;
-    typedef typename TileFor<T, false, false, false>::type ZSmall;
+    typedef typename LogitTile<T, true>::type ZLarge;
+    typedef typename LogitTile<T, false>::type ZSmall;
     typedef typename TileFor<T, true, false, true>::type HLarge;
     typedef typename TileFor<T, true, false, false>::type HSmall;
     typedef typename TileFor<T, true, true, true>::type WLarge;
@@ -987,8 +1080,8 @@ hipError_t head_backward_t(const HeadArgs& a, int dtype, hipStream_t st) {
         head_small_backward_kernel<T><<<dim3((unsigned)(row_wgs + word_wgs)), 256, lds, st>>>(a, row_wgs);
         return hipGetLastError();
     }
-    typedef typename TileFor<T, false, false, true>::type ZLarge;
-    typedef typename TileFor<T, false, false, false>::type ZSmall;
+    typedef typename LogitTile<T, true>::type ZLarge;
+    typedef typename LogitTile<T, false>::type ZSmall;
     typedef typename TileFor<T, true, false, true>::type HLarge;
     typedef typename TileFor<T, true, false, false>::type HSmall;
     typedef typename TileFor<T, true, true, true>::type WLarge;
@@ -998,16 +1091,17 @@ hipError_t head_backward_t(const HeadArgs& a, int dtype, hipStream_t st) {
     const int step = in_place || a.plan.Vg < a.plan.Vw ? a.plan.Vg : a.plan.Vw;
     // grad_hidden's cut serves all pieces (their sums meet): the first is the largest
     const Cut hc = cut_product<HLarge, HSmall>(a.D, a.N, a.V < step ? a.V : step, true, kSumEnds);
-    const hipError_t e = pack_rows<T>(a, cap, a.ghidden && hc.splits == 1, st);
+    const hipError_t e = pack_rows<T>(a, cap, dtype == GR_BF16 ? kPackPlanes : kPackHalves + (a.gweight ? kPackPlanes : 0),
+                                      a.ghidden && hc.splits == 1, st);
     if (e != hipSuccess) return e;
     for (int v = 0; v < a.V; v += step) {
         const int nv = a.V - v < step ? a.V - v : step;
-        const Operand W = words_operand<T>(a, v, nv, dtype, st);
-        if (cut_product<ZLarge, ZSmall>(nv, a.N, a.D, false, kLogitEnds).large) run_grad<ZLarge>(a, W, cap, v, nv, st);
-        else run_grad<ZSmall>(a, W, cap, v, nv, st);
+        const Words W = words_operands<T>(a, v, nv, a.ghidden != nullptr, dtype, st);
+        if (cut_product<ZLarge, ZSmall>(nv, a.N, a.D, false, kLogitEnds).large) run_grad<ZLarge>(a, W.logits, cap, v, nv, st);
+        else run_grad<ZSmall>(a, W.logits, cap, v, nv, st);
         if (a.ghidden) {
-            if (hc.large) run_ghidden<T, HLarge>(a, W, cap, v, nv, hc.splits, st);
-            else run_ghidden<T, HSmall>(a, W, cap, v, nv, hc.splits, st);
+            if (hc.large) run_ghidden<T, HLarge>(a, W.planes, cap, v, nv, hc.splits, st);
+            else run_ghidden<T, HSmall>(a, W.planes, cap, v, nv, hc.splits, st);
         }
         if (a.gweight) {
             const Cut c = cut_product<WLarge, WSmall>(a.D, nv, a.N, true, kSumEnds);
@@ -1029,7 +1123,8 @@ HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool
     p.part_rows = (int32_t)(max_rows < kPartRows ? max_rows : kPartRows);
     p.packed = backward ? max_rows : p.part_rows;
     const int64_t words = round_up(vocab, kWordTile);
-    const int64_t vw = kTableElems / p.planes / p.Dp / kWordTile * kWordTile;
+    p.halves = dtype == GR_BF16 ? 0 : 2;
+    const int64_t vw = kTableElems / (p.planes + p.halves) / p.Dp / kWordTile * kWordTile;
     p.Vw = (int32_t)(vw < kWordTile ? kWordTile : (vw < words ? vw : words));
     p.W = (int64_t)p.planes * p.Vw * p.Dp;
     p.parts = (vocab + kPartWords - 1) / kPartWords * (int64_t)p.part_rows;

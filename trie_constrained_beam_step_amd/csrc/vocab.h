@@ -54,6 +54,7 @@ struct EmbedBackwardArgs {
 // Sizes of a head's workspace, fixed at init for its most rows.
 struct HeadPlan {
     int32_t planes;    // bf16 planes of an element: 1 (bf16) or 3 (fp32)
+    int32_t halves;    // fp16 planes of an element for the logits: 0 (bf16) or 2 (fp32)
     int32_t Dp;        // dim rounded up to 8
     int32_t part_rows; // rows of one forward pass (more go in several)
     int32_t Vg;        // words of a piece of the backward
@@ -73,6 +74,10 @@ struct HeadSpace {
     float* lse;        // [packed row]
     float* zt;         // [packed row] the target's logit
     uint16_t* H;       // [planes][rows][Dp] packed hidden states
+    uint16_t* Hh;      // [halves][rows][Dp] the same, scaled row by row
+    float* hdown;      // [packed row] what divides the row's scale out
+    uint16_t* Wh;      // [halves][Vw][Dp] a piece of the table, scaled word by word
+    float* wdown;      // [Vw] what divides a word's scale out
     float2* parts;     // [parts of the vocabulary][rows] max and sum of 2^(y - max), y = z log2 e
     uint16_t* W;       // [planes][Vw][Dp] a piece of the table, where it cannot be read as it lies
     uint16_t* G;       // [planes][rows][Vg] a piece of the logits' gradient

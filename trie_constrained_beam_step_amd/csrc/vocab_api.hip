@@ -199,7 +199,7 @@ extern "C" void gr_embed_free(gr_embed* h) {
 
 static void head_release(gr_head* h) {
     const gr::HeadSpace& w = h->ws;
-    void* all[] = {w.count, w.target, w.source, w.place, w.gscale, w.lse, w.zt, w.H, w.parts, w.W, w.G, w.gh, w.gw};
+    void* all[] = {w.count, w.target, w.source, w.place, w.gscale, w.lse, w.zt, w.H, w.Hh, w.hdown, w.Wh, w.wdown, w.parts, w.W, w.G, w.gh, w.gw};
     for (void* p : all) (void)hipFree(p);
     delete h;
 }
@@ -224,9 +224,17 @@ extern "C" gr_status gr_head_init(const gr_head_config* cfg, gr_stream stream, g
     if (e == hipSuccess) e = dalloc(&w.source, p.packed);
     if (e == hipSuccess) e = dalloc(&w.place, p.packed);
     if (e == hipSuccess) e = dalloc(&w.zt, p.packed);
-    if (e == hipSuccess) e = dalloc(&w.H, (size_t)p.planes * p.packed * p.Dp);
+    // fp32: the logits take the halves, the gradients the planes
+    const bool planes = !p.halves || !cfg->score_only;
+    if (e == hipSuccess && planes) e = dalloc(&w.H, (size_t)p.planes * p.packed * p.Dp);
+    if (e == hipSuccess && planes) e = dalloc(&w.W, p.W);
+    if (p.halves) {
+        if (e == hipSuccess) e = dalloc(&w.Hh, (size_t)p.halves * p.packed * p.Dp);
+        if (e == hipSuccess) e = dalloc(&w.hdown, p.packed);
+        if (e == hipSuccess) e = dalloc(&w.Wh, (size_t)p.halves * p.Vw * p.Dp);
+        if (e == hipSuccess) e = dalloc(&w.wdown, p.Vw);
+    }
     if (e == hipSuccess) e = dalloc(&w.parts, p.parts);
-    if (e == hipSuccess) e = dalloc(&w.W, p.W);
     if (!cfg->score_only) {
         if (e == hipSuccess) e = dalloc(&w.gscale, p.packed);
         if (e == hipSuccess) e = dalloc(&w.lse, p.packed);
