@@ -144,7 +144,6 @@ __device__ __forceinline__ bool rows_wide(const T* p, int64_t stride) {
     return (uintptr_t)p % 16 == 0 && stride % (16 / (int)sizeof(T)) == 0;
 }
 
-constexpr int kPackRows = 16;  // rows of a workgroup
 // what a packing kernel writes: planes as they are (bf16: one, fp32: three, for
 // the gradients' products), scaled halves (fp32, for the logits)
 constexpr int kPackPlanes = 1, kPackHalves = 2;
@@ -936,7 +935,7 @@ Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split, double ends) {
 constexpr double kLogitEnds = 7, kSumEnds = 4;  // (cut_product) of the logits and of the gradients
 
 constexpr int64_t kPieceElems = 256ll << 20;   // of the logits' gradient at most (512 MB)
-constexpr int64_t kTableElems = 64ll << 20;    // of a packed piece of the table
+constexpr int64_t kTableElems = 128ll << 20;   // of a packed piece of the table, all planes
 constexpr int64_t kPartRows = 65536;           // rows of a forward pass
 constexpr int kWordTile = 256;                 // pieces are whole tiles of any shape
 
@@ -948,8 +947,10 @@ bool reads_in_place(const void* p, int64_t stride, int D, int dtype) {
 
 template <typename T>
 hipError_t pack_rows(const HeadArgs& a, int64_t cap, int what, bool zero_rows, hipStream_t st) {
-    int per = kPackRows;
-    while (tiles_of(a.N, per) > 4096) per *= 2;  // the count before a workgroup's rows is quadratic in their number
+    // a row to a wave while there are few; the counts before the workgroups'
+    // rows are quadratic in the workgroups' number
+    int per = 4;
+    while (tiles_of(a.N, per) > (per < 16 ? 2048 : 4096)) per *= 2;
     pack_rows_kernel<T><<<dim3((unsigned)tiles_of(a.N, per)), 256, 0, st>>>(a, cap, per, what, zero_rows);
     return hipGetLastError();
 }
@@ -1130,7 +1131,8 @@ HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool
     p.parts = (vocab + kPartWords - 1) / kPartWords * (int64_t)p.part_rows;
     if (backward) {
         const int64_t vg = kPieceElems / p.planes / max_rows / kWordTile * kWordTile;
-        const int64_t most_words = vg < kWordTile ? kWordTile : (vg < words ? vg : words);
+        const int64_t fit = vg < p.Vw ? vg : p.Vw;  // fp32 and odd rows: the table's piece is packed
+        const int64_t most_words = fit < kWordTile ? kWordTile : (fit < words ? fit : words);
         // the fewest pieces or up to four more, whichever fills the chip best
         const int64_t fewest = (words + most_words - 1) / most_words;
         double least = 1e300;
