@@ -215,23 +215,39 @@ __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedBackward
         if (i < a.n) atomicAdd(&hist[((keys ? keys[i] : word_of(a, a.tokens[i])) >> shift) & (digits - 1)], 1);
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < digits; d += kSortThreads) a.ws.table[(int64_t)d * nb + blockIdx.x] = hist[d];
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) a.ws.table[(int64_t)blockIdx.x * digits + d] = hist[d];
 }
 
-// A wave per digit: its workgroups' counts become the counts before them.
-__global__ __launch_bounds__(256) void embed_scan_kernel(EmbedBackwardArgs a, int nb, int digits, int own, Fill fill) {
+// Each digit's counts over the workgroups become the counts before them: 16
+// digits to a workgroup, 16 threads to a digit, each a run of the workgroups.
+constexpr int kScanDigits = 16, kScanRuns = 16;
+
+__global__ __launch_bounds__(kScanDigits * kScanRuns) void embed_scan_kernel(EmbedBackwardArgs a, int nb, int digits, int own,
+                                                                             Fill fill) {
+    __shared__ int sums[kScanRuns][kScanDigits];
     if ((int)blockIdx.x >= own) return fill_zeros(a, fill, blockIdx.x - own);
-    const int d = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (d >= digits) return;
-    int32_t* row = a.ws.table + (int64_t)d * nb;
-    int before = 0;
-    for (int b = 0; b < nb; b += 64) {
-        const int x = b + lane < nb ? row[b + lane] : 0;
-        const int inc = (int)wave_inclusive_scan((uint32_t)x);
-        if (b + lane < nb) row[b + lane] = before + inc - x;
-        before += read_lane(inc, 63);
+    const int c = threadIdx.x % kScanDigits, run = threadIdx.x / kScanDigits, d = blockIdx.x * kScanDigits + c;
+    const int per = (nb + kScanRuns - 1) / kScanRuns, b0 = run * per, b1 = min(nb, b0 + per);
+    int sum = 0;
+    if (d < digits)
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) sum += a.ws.table[(int64_t)b * digits + d];
+    sums[run][c] = sum;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int r = 0; r < kScanRuns; ++r) {
+        before += r < run ? sums[r][c] : 0;
+        total += sums[r][c];
     }
-    if (lane == 0) a.ws.totals[d] = before;
+    if (d >= digits) return;
+    if (run == 0) a.ws.totals[d] = total;
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) {
+        int32_t* p = a.ws.table + (int64_t)b * digits + d;
+        const int x = *p;
+        *p = before;
+        before += x;
+    }
 }
 
 __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardArgs a, const int32_t* keys, const int32_t* from,
@@ -255,10 +271,20 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardA
     }
     __syncthreads();
     // where each wave's first position of each digit goes
+    constexpr int kRounds = (1 << kSortBits) / kSortThreads;
+    int totals[kRounds], counts[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int d = r * kSortThreads + threadIdx.x;
+        totals[r] = d < digits ? a.ws.totals[d] : 0;
+        counts[r] = d < digits ? a.ws.table[(int64_t)blockIdx.x * digits + d] : 0;
+    }
     int carry = 0;
-    for (int d0 = 0; d0 < digits; d0 += kSortThreads) {
-        const int d = d0 + threadIdx.x;
-        const int total = d < digits ? a.ws.totals[d] : 0;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int d = r * kSortThreads + threadIdx.x;
+        if (r * kSortThreads >= digits) break;
+        const int total = totals[r];
         const int inc = (int)wave_inclusive_scan((uint32_t)total);
         if (lane == 63) wsum[wave] = inc;
         __syncthreads();
@@ -266,7 +292,7 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardA
         for (int w = 0; w < wave; ++w) before += wsum[w];
         for (int w = 0; w < kSortWaves; ++w) carry += wsum[w];
         if (d < digits) {
-            int o = before + a.ws.table[(int64_t)d * nb + blockIdx.x];
+            int o = before + counts[r];
             for (int w = 0; w < kSortWaves; ++w) {
                 const int c = at[(w << bits) + d];
                 at[(w << bits) + d] = o;
@@ -466,11 +492,11 @@ hipError_t backward_t(const EmbedBackwardArgs& a, hipStream_t st) {
     };
     const int32_t *keys = nullptr, *pos = nullptr;
     for (int q = 0; q < p.passes; ++q) {
-        const int shift = q * p.bits, out = q & 1, digits = 1 << p.bits, scans = (digits + 3) / 4;
+        const int shift = q * p.bits, out = q & 1, digits = 1 << p.bits, scans = (digits + kScanDigits - 1) / kScanDigits;
         int more = share();
         embed_count_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, digits * sizeof(int), st>>>(a, keys, p.blocks, shift, digits, f);
         more = share();
-        embed_scan_kernel<<<dim3((unsigned)(scans + more)), 256, 0, st>>>(a, p.blocks, digits, scans, f);
+        embed_scan_kernel<<<dim3((unsigned)(scans + more)), kScanDigits * kScanRuns, 0, st>>>(a, p.blocks, digits, scans, f);
         more = share();
         embed_move_kernel<<<dim3((unsigned)(p.blocks + more)), kSortThreads, kSortWaves * digits * sizeof(int), st>>>(
             a, keys, pos, a.ws.keys[out], a.ws.pos[out], p.blocks, shift, p.bits, f);

@@ -34,7 +34,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int lanes);
 struct EmbedSpace {
     int32_t* keys[2];  // [n] words in sorted order, by turns
     int32_t* pos[2];   // [n] their positions
-    int32_t* table;    // [digits][workgroups] counts
+    int32_t* table;    // [workgroups][digits] counts
     int32_t* totals;   // [digits]
     float* parts;      // [tiles][2][Dp] sums of words that cross tiles
 };
