@@ -473,7 +473,8 @@ gr_status gr_beam_backward_scatter(gr_beam* beam, int32_t step, const int32_t* d
  *   - Sums are held in 32 bits and each result is rounded once; results do
  *     not depend on scheduling (no floating-point atomics).
  *   - The handle owns its workspace, allocated on the device current at init
- *     by the init call and nowhere else.  The other calls run on that device
+ *     by the init call and nowhere else (nothing is enqueued: `stream` is for
+ *     the init calls' common form).  The other calls run on that device
  *     whatever the current one is, allocate nothing, never synchronise, and
  *     may be captured into a graph.  A handle must not be used from two
  *     threads at once, nor by work that may overlap on the device: two
@@ -509,8 +510,8 @@ gr_status gr_embed_lookup(gr_embed* embed, const int32_t* d_tokens, int32_t n, c
  * every row of [vocab, dim] written (zero where no token is v).  With
  * accumulate != 0 it is added to what d_grad_weight holds (one rounding of
  * the sum), and rows without a token are left as they were.  Each word's
- * rows are summed in fp32 in an order that depends on the tokens alone
- * (ascending i within pieces, pieces in order).
+ * rows are summed in fp32 in an order that depends on the tokens, the sizes
+ * and the rows' alignment alone (ascending i within pieces, pieces in order).
  */
 gr_status gr_embed_backward(gr_embed* embed, const int32_t* d_tokens, int32_t n, const void* d_grad,
                             int64_t grad_row_stride, void* d_grad_weight, int64_t grad_weight_row_stride,
@@ -532,7 +533,9 @@ gr_status gr_head_init(const gr_head_config* cfg, gr_stream stream, gr_head** ou
 /*
  * Softmax cross entropy of rows of hidden states against the head's table,
  * without keeping the logits: with z[n][v] = scale * <hidden[n], weight[v]>
- * (products of the elements summed in fp32),
+ * (products of the elements summed in fp32; fp32 elements enter a product with
+ * 22 bits or more where they are within 2^-17 of their row's largest, and
+ * within 2^-40 of that largest below),
  *   lse[n]  = log sum_v exp(z[n][v])       (the normaliser of a beam step)
  *   loss[n] = lse[n] - z[n][targets[n]]    (-log p of the target)
  * and 0 for both where the target is outside [0, vocab).  d_targets: int32
@@ -550,8 +553,8 @@ gr_status gr_head_loss(gr_head* head, const void* d_hidden, int64_t hidden_row_s
  *   grad_hidden[n] = sum_v G[n][v] * weight[v]     (0 for rows without a target)
  *   grad_weight[v] = sum_n G[n][v] * hidden[n]     (+ what it holds, if accumulate != 0)
  * d_lse is gr_head_loss's of the same inputs.  The logits are computed again,
- * a piece of the vocabulary at a time.  For bf16, a piece's G is rounded to
- * bf16 before both products.  d_grad_hidden or d_grad_weight may be NULL
+ * a piece of the vocabulary at a time.  For bf16, a piece's G may be rounded
+ * to bf16 before both products (half a step of each of its elements).  d_grad_hidden or d_grad_weight may be NULL
  * (not both): that gradient is then not computed.  n = 0 writes zeros to
  * grad_weight unless accumulate.  GR_ERR_UNSUPPORTED for a score_only head.
  */

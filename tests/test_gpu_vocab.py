@@ -201,6 +201,45 @@ def test_head_large(gr, dtype, n, vocab, dim):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_head_more_words_than_a_piece_holds(gr, dtype):
+    """Over two million words for few rows: a row of a piece's gradient stays
+    within the offsets of a tile, so the vocabulary takes several pieces."""
+    n, vocab, dim = 70, 2_200_003, 16
+    h, w, t, g, (hc, gc) = (x if isinstance(x, tuple) else x.cuda() for x in _head_inputs(n, vocab, dim, dtype, 31))
+    want = vu.head(hc.cuda(), w, t, 1.0, dtype, gc.cuda())
+    head = gr.Head(vocab, dim, max_rows=n, dtype=dtype)
+    loss, lse = head.loss(h, w, t)
+    gh, gw = head.backward(h, w, t, lse, g)
+    for name, got in (("loss", loss), ("gh", gh), ("gw", gw)):
+        vu.check(name, got, want[name].cpu(), want[name + "_err"].cpu())
+    head.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [3, 40, 100])
+def test_head_rows_and_words_of_far_sizes(gr, dtype, n):
+    """Rows and words many powers of two apart, and of zeros: each fp32 row is
+    scaled by itself."""
+    vocab, dim = 700, 160
+    h, w, t, g, (hc, gc) = _head_inputs(n, vocab, dim, dtype, 55 + n)
+    size = 2.0 ** torch.randint(-30, 31, (n, 1), generator=_gen(1))
+    back = 2.0 ** torch.randint(-12, 4, (vocab, 1), generator=_gen(2))
+    h, hc = (h.float() * size).to(h.dtype), (hc.float() * size).to(h.dtype)
+    w = (w.float() * back / size.max()).to(w.dtype)
+    hc[n // 2] = 0
+    h[n // 2] = 0
+    w[5] = 0
+    want = vu.head(hc, w, t, 64.0, dtype, gc)
+    head = gr.Head(vocab, dim, max_rows=n, dtype=dtype, scale=64.0)
+    loss, lse = head.loss(h.cuda(), w.cuda(), t.cuda())
+    vu.check("loss", loss, want["loss"], want["loss_err"])
+    gh, gw = head.backward(h.cuda(), w.cuda(), t.cuda(), lse, g.cuda())
+    vu.check("grad_hidden", gh, want["gh"], want["gh_err"])
+    vu.check("grad_weight", gw, want["gw"], want["gw_err"])
+    head.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_head_fewer_rows_than_planned(gr, dtype):
     """One handle, calls of every size up to its most: each as a handle of its own."""
     vocab, dim = 400, 128

@@ -456,7 +456,7 @@ class Embedding(_Table):
         po, so = self._rows(out, "out", n)
         _check(self._lookup(self.handle, pt, n, pw, sw, po, so, self._stream_ptr(stream)))
         if stream is not None:
-            self._used(stream, tokens, weight)
+            self._used(stream, tokens, weight, out)
         return out
 
     def backward(self, tokens, grad, grad_weight=None, accumulate: bool = False, stream=None):
@@ -545,7 +545,7 @@ class Head(_Table):
                 grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, stream)
             pgw, sgw = self._rows(grad_weight, "grad_weight", self.vocab)
         _check(self._backward(self.handle, ph, sh, pw, sw, pt, n, pl, pg, pgh, sgh, pgw, sgw,
-                                      1 if accumulate else 0, self._stream_ptr(stream)))
+                              1 if accumulate else 0, self._stream_ptr(stream)))
         if stream is not None:
             self._used(stream, hidden, weight, targets, lse, grad_loss, grad_hidden, grad_weight)
         return grad_hidden, grad_weight

@@ -1131,8 +1131,9 @@ HeadPlan head_plan(int64_t max_rows, int64_t vocab, int64_t dim, int dtype, bool
     p.parts = (vocab + kPartWords - 1) / kPartWords * (int64_t)p.part_rows;
     if (backward) {
         const int64_t vg = kPieceElems / p.planes / max_rows / kWordTile * kWordTile;
-        const int64_t fit = vg < p.Vw ? vg : p.Vw;  // fp32 and odd rows: the table's piece is packed
-        const int64_t most_words = fit < kWordTile ? kWordTile : (fit < words ? fit : words);
+        // fp32 and odd rows: the table's piece is packed; a row of G is an operand's
+        const int64_t fit = vg < p.Vw ? vg : p.Vw, whole = words < kMaxTileStride ? words : kMaxTileStride;
+        const int64_t most_words = fit < kWordTile ? kWordTile : (fit < whole ? fit : whole);
         // the fewest pieces or up to four more, whichever fills the chip best
         const int64_t fewest = (words + most_words - 1) / most_words;
         double least = 1e300;

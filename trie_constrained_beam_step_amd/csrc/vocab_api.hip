@@ -56,6 +56,7 @@ gr_status check_count(int32_t n, int32_t most) {
     return GR_OK;
 }
 
+// dtype of the elements; GR_F32 stands for any 32-bit type
 gr_status check_aligned(const void* p, int32_t dtype, const char* what) {
     if ((uintptr_t)p % (dtype == GR_BF16 ? 2 : 4)) return fail(GR_ERR_INVALID_ARG, "%s is not aligned to its elements", what);
     return GR_OK;
@@ -143,6 +144,7 @@ extern "C" gr_status gr_embed_lookup(gr_embed* h, const int32_t* d_tokens, int32
     GR_TRY(check_stride(&out_row_stride, c.dim, "out"));
     GR_TRY(check_aligned(d_weight, c.dtype, "weight"));
     GR_TRY(check_aligned(d_out, c.dtype, "out"));
+    GR_TRY(check_aligned(d_tokens, GR_F32, "tokens"));
     gr::EmbedLookupArgs a;
     a.tokens = d_tokens;
     a.n = n;
@@ -169,6 +171,7 @@ extern "C" gr_status gr_embed_backward(gr_embed* h, const int32_t* d_tokens, int
     GR_TRY(check_stride(&grad_weight_row_stride, c.dim, "grad_weight"));
     GR_TRY(check_aligned(d_grad, c.dtype, "grad"));
     GR_TRY(check_aligned(d_grad_weight, c.dtype, "grad_weight"));
+    GR_TRY(check_aligned(d_tokens, GR_F32, "tokens"));
     gr::EmbedBackwardArgs a;
     a.tokens = d_tokens;
     a.n = n;
@@ -272,6 +275,9 @@ extern "C" gr_status gr_head_loss(gr_head* h, const void* d_hidden, int64_t hidd
     GR_TRY(check_stride(&weight_row_stride, c.dim, "weight"));
     GR_TRY(check_aligned(d_hidden, c.dtype, "hidden"));
     GR_TRY(check_aligned(d_weight, c.dtype, "weight"));
+    GR_TRY(check_aligned(d_targets, GR_F32, "targets"));
+    GR_TRY(check_aligned(d_loss, GR_F32, "loss"));
+    GR_TRY(check_aligned(d_lse, GR_F32, "lse"));
     gr::HeadArgs a = head_args(h, n);
     a.hidden = d_hidden;
     a.hstride = hidden_row_stride;
@@ -305,6 +311,9 @@ extern "C" gr_status gr_head_backward(gr_head* h, const void* d_hidden, int64_t 
     GR_TRY(check_aligned(d_weight, c.dtype, "weight"));
     GR_TRY(check_aligned(d_grad_hidden, c.dtype, "grad_hidden"));
     GR_TRY(check_aligned(d_grad_weight, c.dtype, "grad_weight"));
+    GR_TRY(check_aligned(d_targets, GR_F32, "targets"));
+    GR_TRY(check_aligned(d_lse, GR_F32, "lse"));
+    GR_TRY(check_aligned(d_grad_loss, GR_F32, "grad_loss"));
     gr::HeadArgs a = head_args(h, n);
     a.hidden = d_hidden;
     a.hstride = hidden_row_stride;
