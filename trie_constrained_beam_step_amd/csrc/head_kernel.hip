@@ -464,17 +464,17 @@ struct Raw8<float> {
     }
 };
 
-template <typename T, int FN, int Waves, int StepK>
-__global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
-    static_assert(Waves * 16 >= kPartWords, "a part for each workgroup");
-    constexpr int NT = Waves * 64;
+template <typename T, int FN, int MinWaves, int MaxWaves, int StepK>
+__global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) {
+    static_assert(MinWaves * 16 >= kPartWords, "a part for each workgroup");
+    const int NT = blockDim.x, waves = NT / 64;  // MinWaves .. MaxWaves
     constexpr int PL = sizeof(T) == 2 ? 1 : 3, kRows = FN * 16, kChunks = StepK / 8;
-    constexpr int kItems = (kRows * kChunks + NT - 1) / NT, kParts32 = StepK / 32;
+    constexpr int kItems = (kRows * kChunks + MinWaves * 64 - 1) / (MinWaves * 64), kParts32 = StepK / 32;
     __shared__ __align__(16) uint16_t hs[2][PL][kRows][StepK];
-    __shared__ float sm[Waves][kRows], ss[Waves][kRows];
+    __shared__ float sm[MaxWaves][kRows], ss[MaxWaves][kRows];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool hwide = rows_wide((const T*)a.hidden, a.hstride), wwide = rows_wide((const T*)a.weight, a.wstride);
-    const int v0 = (blockIdx.x * Waves + wave) * 16;
+    const int v0 = (blockIdx.x * waves + wave) * 16;
     const int steps = tiles_of(a.D, StepK);
     // the width is walked in a circle from another step in every workgroup: rows
     // of the table lie a power of two apart as often as not, and workgroups in
@@ -596,8 +596,8 @@ __global__ __launch_bounds__(Waves * 64) void head_stream_kernel(HeadArgs a) {
     if ((int)threadIdx.x < kRows && (int)threadIdx.x < a.N) {
         const int n = threadIdx.x;
         float m = sm[0][n], s = 0.0f;
-        for (int w = 1; w < Waves; ++w) m = fmaxf(m, sm[w][n]);
-        for (int w = 0; w < Waves; ++w) s += ss[w][n] * ex2(sm[w][n] - m);
+        for (int w = 1; w < waves; ++w) m = fmaxf(m, sm[w][n]);
+        for (int w = 0; w < waves; ++w) s += ss[w][n] * ex2(sm[w][n] - m);
         a.ws.parts[(int64_t)blockIdx.x * a.N + n] = make_float2(m, s);
     }
 }
@@ -995,15 +995,26 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
         a.lse = all.lse + r;
         a.grad_loss = nullptr;
         if (a.N <= kFewRows) {
-            // more rows: more waves share the staging of the hidden states, which
+            // More rows: more waves share the staging of the hidden states, which
             // fp32 pays most for (64 rows of 50,257 x 768: 16 waves 46 us, 4 waves
-            // 65; one row of 151,936 x 2,048 bf16: 132 and 123 us)
+            // 65; one row of 151,936 x 2,048 bf16: 132 and 123 us); 8 to 16 of
+            // them, as many as fill the last round of workgroups best.
             constexpr int kWide = 256 / sizeof(T);  // 256 bytes of a row a step: 116 us, 128 bytes 122, 512 bytes 120
-            const int waves = a.N <= 16 ? 4 : 16;
-            const unsigned wgs = (unsigned)tiles_of(a.V, waves * 16);
-            if (a.N <= 16) head_stream_kernel<T, 1, 4, kWide><<<dim3(wgs), 256, 0, st>>>(a);
-            else if (a.N <= 32) head_stream_kernel<T, 2, 16, 64><<<dim3(wgs), 1024, 0, st>>>(a);
-            else head_stream_kernel<T, 4, 16, 64><<<dim3(wgs), 1024, 0, st>>>(a);
+            int waves = 4;
+            if (a.N > 16) {
+                int64_t least = INT64_MAX;
+                for (int w = 16; w >= 8; --w) {
+                    const int64_t c = (int64_t)tiles_of(tiles_of(a.V, w * 16), kCUs) * w;
+                    if (c < least) {
+                        least = c;
+                        waves = w;
+                    }
+                }
+            }
+            const unsigned wgs = (unsigned)tiles_of(a.V, waves * 16), threads = waves * 64;
+            if (a.N <= 16) head_stream_kernel<T, 1, 4, 4, kWide><<<dim3(wgs), threads, 0, st>>>(a);
+            else if (a.N <= 32) head_stream_kernel<T, 2, 8, 16, 64><<<dim3(wgs), threads, 0, st>>>(a);
+            else head_stream_kernel<T, 4, 8, 16, 64><<<dim3(wgs), threads, 0, st>>>(a);
             head_join_kernel<<<dim3((unsigned)a.N), 1024, 0, st>>>(a, a.N, (int)wgs, 1, false);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
