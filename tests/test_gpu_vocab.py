@@ -427,6 +427,127 @@ def test_on_a_side_stream_and_replayed_from_a_graph(gr, dtype):
     emb.close(), head.close()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(150, 300), (700, 900)])
+def test_replay_reads_what_the_buffers_hold(gr, dtype, n, vocab):
+    """A captured step replayed on other inputs, with another number of rows that
+    have a target (none and all among them), is the eager step on those."""
+    dim = 128
+    emb = gr.Embedding(vocab, dim, max_tokens=n, dtype=dtype)
+    head = gr.Head(vocab, dim, max_rows=n, dtype=dtype)
+    h, w, t, g = (torch.zeros(s, dtype=d, device="cuda") for s, d in
+                  (((n, dim), vu.DT[dtype]), ((vocab, dim), vu.DT[dtype]), ((n,), torch.int32), ((n,), torch.float32)))
+
+    def step():
+        loss, lse = head.loss(h, w, t)
+        gh, gw = head.backward(h, w, t, lse, g)
+        return loss, lse, gh, gw, emb.lookup(t, w), emb.backward(t, gh)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i, absent in enumerate((0.2, 1.0, 0.0, 0.6)):
+        hh, ww, tt, gg, _ = _head_inputs(n, vocab, dim, dtype, 40 + i, absent)
+        for dst, src in ((h, hh), (w, ww), (t, tt), (g, gg)):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for k, (a, b) in enumerate(zip(got, step())):
+            assert torch.equal(a, b), f"replay {i}, output {k}"
+    emb.close(), head.close()
+
+
+def test_two_handles_on_two_streams(gr):
+    """Handles do not share workspaces: work of two of them may overlap."""
+    n, vocab, dim = 900, 3000, 256
+    data = [_head_inputs(n, vocab, dim, "bf16", s) for s in (1, 2)]
+    data = [tuple(x.cuda() for x in d[:4]) for d in data]
+    heads = [gr.Head(vocab, dim, max_rows=n, dtype="bf16") for _ in data]
+    embs = [gr.Embedding(vocab, dim, max_tokens=n, dtype="bf16") for _ in data]
+
+    def step(i, stream=None):
+        h, w, t, g = data[i]
+        loss, lse = heads[i].loss(h, w, t, stream=stream)
+        gh, gw = heads[i].backward(h, w, t, lse, g, stream=stream)
+        return loss, gh, gw, embs[i].backward(t, gh, stream=stream)
+
+    alone = [step(i) for i in (0, 1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    for _ in range(3):
+        both = [step(i, streams[i]) for i in (0, 1)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+    for x in (*heads, *embs):
+        x.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [65_546, 70_000])
+def test_head_more_rows_than_a_pass(gr, dtype, n):
+    """More rows than one pass of the loss takes: the last pass is of few rows or
+    of many."""
+    vocab, dim = 200, 24
+    h, w, t, g, (hc, gc) = (x if isinstance(x, tuple) else x.cuda() for x in _head_inputs(n, vocab, dim, dtype, 6))
+    want = vu.head(hc.cuda(), w, t, 1.0, dtype, gc.cuda())
+    head = gr.Head(vocab, dim, max_rows=n, dtype=dtype)
+    loss, lse = head.loss(h, w, t)
+    gh, gw = head.backward(h, w, t, lse, g)
+    for name, got in (("loss", loss), ("lse", lse), ("gh", gh), ("gw", gw)):
+        vu.check(name, got, want[name].cpu(), want[name + "_err"].cpu())
+    head.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab,dim,scale", [(70, 90, 20_000, 1.0), (5, 40, 20_000, 1.0), (100, 300, 64, -0.75),
+                                               (20, 300, 64, -0.75), (100, 300, 64, 1e-20), (3, 300, 64, 1e-20)])
+def test_head_wide_rows_and_odd_scales(gr, dtype, n, vocab, dim, scale):
+    scale = float(np.float32(scale))
+    h, w, t, g, (hc, gc) = _head_inputs(n, vocab, dim, dtype, 3)
+    want = vu.head(hc, w, t, scale, dtype, gc)
+    head = gr.Head(vocab, dim, max_rows=n, dtype=dtype, scale=scale)
+    loss, lse = head.loss(h.cuda(), w.cuda(), t.cuda())
+    gh, gw = head.backward(h.cuda(), w.cuda(), t.cuda(), lse, g.cuda())
+    for name, got in (("loss", loss), ("lse", lse), ("gh", gh), ("gw", gw)):
+        vu.check(name, got, want[name], want[name + "_err"])
+    head.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [7, 100, 1500])
+def test_scoring_head_is_the_training_heads_loss(gr, dtype, n):
+    h, w, t, g, _ = _head_inputs(n, 1000, 100, dtype, 8)
+    h, w, t = h.cuda(), w.cuda(), t.cuda()
+    full, score = (gr.Head(1000, 100, max_rows=n, dtype=dtype, backward=b) for b in (True, False))
+    for a, b in zip(full.loss(h, w, t), score.loss(h, w, t)):
+        assert torch.equal(a, b)
+    full.close(), score.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab,dim", [(1_200_000, 70_000, 8), (3000, 5_000_000, 4), (20_000, 5000, 1024), (513, 2047, 8),
+                                         (600, 2048, 8), (900, 3, 6000)])
+def test_embedding_of_many(gr, dtype, n, vocab, dim):
+    """Sorts of one, two and three passes, tiles of more than a few rows, whole
+    rows to a thread group, and lookups of four rows a group."""
+    gen = _gen(n)
+    t = _tokens(n, vocab, gen, 0.1)
+    ok = (t >= 0) & (t < vocab)
+    w = torch.randn(vocab, dim, generator=gen).to(vu.DT[dtype])
+    g = torch.randn(n, dim, generator=gen).to(vu.DT[dtype])
+    e = gr.Embedding(vocab, dim, max_tokens=n, dtype=dtype, scale=0.5)
+    want = torch.where(ok[:, None], w[t.clamp(0, vocab - 1).long()].float() * 0.5, 0.0).to(vu.DT[dtype])
+    assert torch.equal(e.lookup(t.cuda(), w.cuda()).cpu(), want)
+    ref, err = vu.scatter(t, g, vocab, 0.5, dtype)
+    vu.check("grad_weight", e.backward(t.cuda(), g.cuda()), ref, err)
+    e.close()
+
+
 def test_refusals(gr):
     E, H = gr.Embedding(40, 16, max_tokens=8), gr.Head(40, 16, max_rows=8, dtype="bf16")
     w = torch.zeros(40, 16, device="cuda")
