@@ -915,14 +915,15 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
 
 constexpr int kMaxSplits = 64;
 constexpr int kCUs = 256;
+constexpr int kLdsBytes = 160 << 10;  // of a CU
 
 // How a product of m x n with k steps is cut: into large or small tiles, the k
 // axis into splits.  The cost is in k steps of a large tile: rounds of
 // workgroups over the chip, each its k steps and `ends` more for its first
-// loads and its epilogue; two small tiles (half a large bf16 tile's work
-// together) share a CU at four fifths of the large tile's rate.  Splits pay
-// for writing and reading their fp32 sums: a CU moves a large tile's in about
-// six k steps.
+// loads and its epilogue; small tiles work at four fifths of the large ones'
+// rate, two of them share a CU where their LDS allows.  Splits pay for writing
+// and reading their fp32 sums: a CU moves a large tile's in about six k steps,
+// and the launch that adds them takes about two and a half.  Only splits that fill one, two or three rounds can be the best.
 struct Cut {
     bool large;
     int splits;
@@ -932,20 +933,27 @@ constexpr int kMostRounds = 3;  // of a split product
 
 template <typename Large, typename Small>
 Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split, double ends) {
-    constexpr double kSmallStep = 2.0 * Small::BM * Small::BN / (Large::BM * Large::BN) / 0.8;
-    const int64_t steps = (k + Large::BK - 1) / Large::BK;
+    constexpr int kSmallShare = 4 * Small::Stage <= kLdsBytes ? 2 : 1;  // small tiles on a CU
+    constexpr double kSmallStep = (double)kSmallShare * Small::BM * Small::BN / (Large::BM * Large::BN) / 0.8;
+    const int steps = tiles_of(k, Large::BK);
     Cut best{true, 1, 1e300};
     for (int large = 1; large >= 0; --large) {
         const int64_t tiles = large ? (int64_t)tiles_of(m, Large::BM) * tiles_of(n, Large::BN)
                                     : (int64_t)tiles_of(m, Small::BM) * tiles_of(n, Small::BN);
-        const int64_t slots = large ? kCUs : 2 * kCUs;
+        const int slots = large ? kCUs : kSmallShare * kCUs;
         const double step = large ? 1.0 : kSmallStep;
-        for (int s = 1; s <= (may_split ? kMaxSplits : 1); ++s) {
-            if (s > 1 && (tiles * s > kMostRounds * slots || steps / s < 4)) break;
+        for (int round = 0; round <= (may_split ? kMostRounds : 0); ++round) {
+            int64_t s = 1;
+            if (round > 0) {
+                s = (int64_t)round * slots / tiles;
+                if (s > kMaxSplits) s = kMaxSplits;
+                if (s > steps / 4) s = steps / 4;  // four k steps each, or more
+                if (s < 2) continue;
+            }
             const double rounds = (double)((tiles * s + slots - 1) / slots);
-            double cost = rounds * (((steps + s - 1) / s) + ends) * step;
-            if (s > 1) cost += 6.0 * step * (double)(tiles * s) / slots;
-            if (cost < best.cost * 0.999) best = Cut{large != 0, s, cost};
+            double cost = rounds * ((double)((steps + s - 1) / s) + ends) * step;
+            if (s > 1) cost += 6.0 * step * (double)(tiles * s) / slots + 2.5;
+            if (cost < best.cost * 0.999) best = Cut{large != 0, (int)s, cost};
         }
     }
     return best;
