@@ -345,6 +345,9 @@ class _Table:
         self._torch_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self._gr_dtype = _lib.GR_BF16 if dtype == "bf16" else _lib.GR_F32
         self._torch = torch
+        # the current stream's address without a Stream object, where torch has it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
         self._h = None
 
     def _made(self, handle):
@@ -367,7 +370,8 @@ class _Table:
 
     def _flat(self, t, name, dtype, n=None):
         """A contiguous tensor (of n elements): its address."""
-        self._tensor(t, name, dtype)
+        if not isinstance(t, self._torch.Tensor) or t.dtype is not dtype or t.get_device() != self._index:
+            self._tensor(t, name, dtype)
         if not t.is_contiguous() or (n is not None and t.numel() != n):
             raise ValueError(f"{name} must be contiguous" + (f" with {n} elements" if n is not None else ""))
         return t.data_ptr()
@@ -375,7 +379,8 @@ class _Table:
     def _rows(self, t, name, n):
         """n rows of `dim` elements, [n, dim] with any row stride or contiguous
         [..., dim]: their address and row stride."""
-        self._tensor(t, name, self._torch_dtype)
+        if not isinstance(t, self._torch.Tensor) or t.dtype is not self._torch_dtype or t.get_device() != self._index:
+            self._tensor(t, name, self._torch_dtype)
         dim = self.dim
         if t.dim() < 2 or t.shape[-1] != dim or t.numel() != n * dim:
             raise ValueError(f"{name} must hold {n} rows of {dim}, not {tuple(t.shape)}")
@@ -397,7 +402,7 @@ class _Table:
         """The address of the stream to enqueue on (default: torch's current one
         of the handle's device)."""
         if stream is None:
-            return self._torch.cuda.current_stream(self._index).cuda_stream
+            return self._current(self._index)
         return self._stream(stream).cuda_stream
 
     def _empty(self, shape, dtype, stream):
@@ -453,7 +458,9 @@ class Embedding(_Table):
         pw, sw = self._rows(weight, "weight", self.vocab)
         if out is None:
             out = self._empty((*tokens.shape, self.dim), self._torch_dtype, stream)
-        po, so = self._rows(out, "out", n)
+            po, so = out.data_ptr(), self.dim
+        else:
+            po, so = self._rows(out, "out", n)
         _check(self._lookup(self.handle, pt, n, pw, sw, po, so, self._stream_ptr(stream)))
         if stream is not None:
             self._used(stream, tokens, weight, out)
@@ -471,7 +478,9 @@ class Embedding(_Table):
             if accumulate:
                 raise ValueError("accumulate needs the grad_weight to add to")
             grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, stream)
-        pw, sw = self._rows(grad_weight, "grad_weight", self.vocab)
+            pw, sw = grad_weight.data_ptr(), self.dim
+        else:
+            pw, sw = self._rows(grad_weight, "grad_weight", self.vocab)
         _check(self._backward(self.handle, pt, n, pg, sg, pw, sw, 1 if accumulate else 0, self._stream_ptr(stream)))
         if stream is not None:
             self._used(stream, tokens, grad, grad_weight)
@@ -525,8 +534,7 @@ class Head(_Table):
         pw, sw = self._rows(weight, "weight", self.vocab)
         pl = self._flat(lse, "lse", torch.float32, n)
         pg = self._flat(grad_loss, "grad_loss", torch.float32, n)
-        need = set(need)
-        if not need or not need <= {"hidden", "weight"}:
+        if not need or any(x not in ("hidden", "weight") for x in need):
             raise ValueError("need names 'hidden', 'weight' or both")
         pgh = pgw = None
         sgh = sgw = 0
@@ -535,7 +543,9 @@ class Head(_Table):
         else:
             if grad_hidden is None:
                 grad_hidden = self._empty(hidden.shape, self._torch_dtype, stream)
-            pgh, sgh = self._rows(grad_hidden, "grad_hidden", n)
+                pgh, sgh = grad_hidden.data_ptr(), self.dim
+            else:
+                pgh, sgh = self._rows(grad_hidden, "grad_hidden", n)
         if "weight" not in need:
             grad_weight = None
         else:
@@ -543,7 +553,9 @@ class Head(_Table):
                 if accumulate:
                     raise ValueError("accumulate needs the grad_weight to add to")
                 grad_weight = self._empty((self.vocab, self.dim), self._torch_dtype, stream)
-            pgw, sgw = self._rows(grad_weight, "grad_weight", self.vocab)
+                pgw, sgw = grad_weight.data_ptr(), self.dim
+            else:
+                pgw, sgw = self._rows(grad_weight, "grad_weight", self.vocab)
         _check(self._backward(self.handle, ph, sh, pw, sw, pt, n, pl, pg, pgh, sgh, pgw, sgw,
                               1 if accumulate else 0, self._stream_ptr(stream)))
         if stream is not None:

@@ -1027,7 +1027,7 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
             // 65; one row of 151,936 x 2,048 bf16: 132 and 123 us); 8 to 16 of
             // them, as many as fill the last round of workgroups best.
             constexpr int kWide = 256 / sizeof(T);  // 256 bytes of a row a step: 116 us, 128 bytes 122, 512 bytes 120
-            int waves = 4;
+            int waves = a.N <= 4 ? 4 : 8;  // 16 rows of 151,936 x 1,024: 8 waves 62 us, 4 waves 66; one row of 2,048: 117 and 115
             if (a.N > 16) {
                 int64_t least = INT64_MAX;
                 for (int w = 16; w >= 8; --w) {
@@ -1039,7 +1039,7 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
                 }
             }
             const unsigned wgs = (unsigned)tiles_of(a.V, waves * 16), threads = waves * 64;
-            if (a.N <= 16) head_stream_kernel<T, 1, 4, 4, kWide><<<dim3(wgs), threads, 0, st>>>(a);
+            if (a.N <= 16) head_stream_kernel<T, 1, 4, 8, kWide><<<dim3(wgs), threads, 0, st>>>(a);
             else if (a.N <= 32) head_stream_kernel<T, 2, 8, 16, 64><<<dim3(wgs), threads, 0, st>>>(a);
             else head_stream_kernel<T, 4, 8, 16, 64><<<dim3(wgs), threads, 0, st>>>(a);
             head_join_kernel<<<dim3((unsigned)a.N), 1024, 0, st>>>(a, a.N, (int)wgs, 1, false);
