@@ -548,6 +548,22 @@ def test_embedding_of_many(gr, dtype, n, vocab, dim):
     e.close()
 
 
+def test_workspace_that_does_not_fit(gr):
+    """An allocation that fails is an error of init; nothing of it stays behind."""
+    free = torch.cuda.mem_get_info()[0]
+    with pytest.raises(gr.GrError) as e:
+        gr.Head(1 << 30, 64, max_rows=1 << 20, dtype="bf16")  # 8 TB of parts
+    assert e.value.status == gr._lib.GR_ERR_OUT_OF_MEMORY
+    torch.cuda.synchronize()
+    assert torch.cuda.mem_get_info()[0] >= free - (64 << 20)
+    head = gr.Head(48, 64, max_rows=4)
+    x = torch.zeros(4, 64, device="cuda")
+    loss, _ = head.loss(x, torch.zeros(48, 64, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda"))
+    # log 48 within fp32 roundings of a sum of 48 ones and a logarithm
+    assert abs(float(loss[0]) - float(np.log(48.0))) < 1e-5
+    head.close()
+
+
 def test_refusals(gr):
     E, H = gr.Embedding(40, 16, max_tokens=8), gr.Head(40, 16, max_rows=8, dtype="bf16")
     w = torch.zeros(40, 16, device="cuda")

@@ -395,6 +395,9 @@ __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operan
     }
 }
 
+// The normaliser from a row's maximum and sum in units of log 2.
+__device__ __forceinline__ float lse_of(float m, float s) { return (float)(kLn2 * ((double)m + (double)log2f(s))); }
+
 // Loss and lse of each row from its parts: workgroups of `rb` rows, 1024 / rb
 // threads to a row.  packed: the rows are pack_rows_kernel's.
 __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t rows_cap, int parts, int rb, bool packed) {
@@ -424,7 +427,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(HeadArgs a, int64_t row
     if (slice == 0 && n < a.N) {
         float lse = 0.0f, loss = 0.0f;
         if (at >= 0) {
-            lse = (float)(kLn2 * ((double)sm[row] + (double)log2f(ss[row])));
+            lse = lse_of(sm[row], ss[row]);
             loss = lse - a.ws.zt[at];
         }
         a.loss[n] = loss;
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) 
     constexpr int PL = sizeof(T) == 2 ? 1 : 3, kRows = FN * 16, kChunks = StepK / 8;
     constexpr int kItems = (kRows * kChunks + MinWaves * 64 - 1) / (MinWaves * 64), kParts32 = StepK / 32;
     __shared__ __align__(16) uint16_t hs[2][PL][kRows][StepK];
-    __shared__ float sm[MaxWaves][kRows], ss[MaxWaves][kRows];
+    __shared__ float sm[MaxWaves][kRows], ss[MaxWaves][kRows], szt[kRows];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool hwide = rows_wide((const T*)a.hidden, a.hstride), wwide = rows_wide((const T*)a.weight, a.wstride);
     const int v0 = (blockIdx.x * waves + wave) * 16;
@@ -588,7 +591,7 @@ __global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) 
         float m = kFarBelow, s = 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (t == r) a.ws.zt[n] = acc[j][r] * a.scale;
+            if (t == r) szt[n] = acc[j][r] * a.scale;  // at most one lane of the workgroup
             acc[j][r] *= a.scale * kLog2e;
             if (v0 + (lane >> 4) * 4 + r < a.V) m = fmaxf(m, acc[j][r]);
         }
@@ -610,7 +613,15 @@ __global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) 
         float m = sm[0][n], s = 0.0f;
         for (int w = 1; w < waves; ++w) m = fmaxf(m, sm[w][n]);
         for (int w = 0; w < waves; ++w) s += ss[w][n] * ex2(sm[w][n] - m);
+        const int t = has_target(a, n) ? a.targets[n] : -1;
+        if (gridDim.x == 1) {  // the whole vocabulary: nothing to join
+            const float lse = t < 0 ? 0.0f : lse_of(m, s);
+            a.lse[n] = lse;
+            a.loss[n] = t < 0 ? 0.0f : lse - szt[n];
+            return;
+        }
         a.ws.parts[(int64_t)blockIdx.x * a.N + n] = make_float2(m, s);
+        if (t >= 0 && t / (waves * 16) == (int)blockIdx.x) a.ws.zt[n] = szt[n];
     }
 }
 
@@ -1042,7 +1053,7 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
             if (a.N <= 16) head_stream_kernel<T, 1, 4, 8, kWide><<<dim3(wgs), threads, 0, st>>>(a);
             else if (a.N <= 32) head_stream_kernel<T, 2, 8, 16, 64><<<dim3(wgs), threads, 0, st>>>(a);
             else head_stream_kernel<T, 4, 8, 16, 64><<<dim3(wgs), threads, 0, st>>>(a);
-            head_join_kernel<<<dim3((unsigned)a.N), 1024, 0, st>>>(a, a.N, (int)wgs, 1, false);
+            if (wgs > 1) head_join_kernel<<<dim3((unsigned)a.N), 1024, 0, st>>>(a, a.N, (int)wgs, 1, false);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
             continue;
