@@ -2,8 +2,7 @@
 // table's gradient from those rows' gradient.
 //
 // Both move rows and add little: they are bound by HBM.  A row is read and
-// written 16 bytes a thread (one element a thread where the rows do not start
-// on 16 bytes), `lanes` threads to a row.
+// written 16 bytes a thread, `lanes` threads to a row.
 //
 // The gradient has one writer per word and no floating-point atomics.  Few
 // tokens (embed_few_kernel): one launch, each workgroup collects its words'
@@ -23,60 +22,85 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// N consecutive elements: 16 bytes of them, or one.  Raw is how they are loaded,
-// value(raw, e) element e as fp32.
-template <typename T, int N>
-struct Pack;
+// 16 bytes of a row's elements, kElems of them; `left` of the row's exist.  Raw is
+// how they are loaded, value(raw, e) element e as fp32.  Rows need no alignment
+// beyond the element's: the hardware takes 16-byte accesses anywhere.
 template <typename T>
-struct Pack<T, 1> {
-    typedef T Raw;
-    static __device__ __forceinline__ Raw raw(const T* p) { return *p; }
-    static __device__ __forceinline__ float value(const Raw& r, int) { return load_elem(&r, 0); }
-    static __device__ __forceinline__ void store(float* p, const float (&x)[1]) { *p = x[0]; }
-    static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[1]) { *p = bf16_bits(x[0]); }
-};
+struct Pack;
 template <>
-struct Pack<float, 4> {
+struct Pack<float> {
+    static constexpr int kElems = 4;
     typedef f32x4v Raw;
-    static __device__ __forceinline__ Raw raw(const float* p) { return *(const f32x4v*)p; }
+    typedef f32x4v Anywhere __attribute__((aligned(4)));
+    static __device__ __forceinline__ Raw raw(const float* p, int left) {
+        if (left >= 4) return *(const Anywhere*)p;
+        Raw r = {};
+        #pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) r[e] = p[e];
+        return r;
+    }
     static __device__ __forceinline__ float value(const Raw& r, int e) { return r[e]; }
-    static __device__ __forceinline__ void store(float* p, const float (&x)[4]) { *(f32x4v*)p = f32x4v{x[0], x[1], x[2], x[3]}; }
+    static __device__ __forceinline__ void store(float* p, int left, const float (&x)[4]) {
+        if (left >= 4) {
+            *(Anywhere*)p = f32x4v{x[0], x[1], x[2], x[3]};
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) p[e] = x[e];
+    }
 };
 template <>
-struct Pack<uint16_t, 8> {
+struct Pack<uint16_t> {
+    static constexpr int kElems = 8;
     typedef u32x4 Raw;
-    static __device__ __forceinline__ Raw raw(const uint16_t* p) { return *(const u32x4*)p; }
+    typedef u32x4 Anywhere __attribute__((aligned(2)));
+    static __device__ __forceinline__ Raw raw(const uint16_t* p, int left) {
+        if (left >= 8) return *(const Anywhere*)p;
+        Raw r = {};
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) r[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        return r;
+    }
     static __device__ __forceinline__ float value(const Raw& r, int e) {
         return __uint_as_float(e & 1 ? r[e >> 1] & 0xFFFF0000u : r[e >> 1] << 16);
     }
-    static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[8]) {
-        u32x4 v;
+    static __device__ __forceinline__ void store(uint16_t* p, int left, const float (&x)[8]) {
+        if (left >= 8) {
+            u32x4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = bf16_bits(x[2 * e]) | (uint32_t)bf16_bits(x[2 * e + 1]) << 16;
-        *(u32x4*)p = v;
+            for (int e = 0; e < 4; ++e) v[e] = bf16_bits(x[2 * e]) | (uint32_t)bf16_bits(x[2 * e + 1]) << 16;
+            *(Anywhere*)p = v;
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) p[e] = bf16_bits(x[e]);
     }
 };
 
 // Writes a word's sum: scaled, or added to what its row holds.
-template <typename T, int N>
+template <typename T, int N = Pack<T>::kElems>
 __device__ __forceinline__ void put_word(const EmbedBackwardArgs& a, int v, int d, float (&s)[N]) {
     T* o = (T*)a.gweight + (int64_t)v * a.wstride + d;
     if (a.accumulate) {
-        const typename Pack<T, N>::Raw old = Pack<T, N>::raw(o);
+        const typename Pack<T>::Raw old = Pack<T>::raw(o, a.D - d);
 #pragma unroll
-        for (int e = 0; e < N; ++e) s[e] = fmaf(s[e], a.scale, Pack<T, N>::value(old, e));
+        for (int e = 0; e < N; ++e) s[e] = fmaf(s[e], a.scale, Pack<T>::value(old, e));
     } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) s[e] *= a.scale;
     }
-    Pack<T, N>::store(o, s);
+    Pack<T>::store(o, a.D - d, s);
 }
 
-template <typename T, int N>
+template <typename T, int N = Pack<T>::kElems>
 __device__ __forceinline__ void add_row(const EmbedBackwardArgs& a, int i, int d, float (&s)[N]) {
-    const typename Pack<T, N>::Raw x = Pack<T, N>::raw((const T*)a.grad + (int64_t)i * a.gstride + d);
+    const typename Pack<T>::Raw x = Pack<T>::raw((const T*)a.grad + (int64_t)i * a.gstride + d, a.D - d);
 #pragma unroll
-    for (int e = 0; e < N; ++e) s[e] += Pack<T, N>::value(x, e);
+    for (int e = 0; e < N; ++e) s[e] += Pack<T>::value(x, e);
 }
 
 constexpr int kFewWords = 512;  // words of an embed_few_kernel workgroup at most
@@ -88,25 +112,26 @@ __device__ __forceinline__ bool in_table(int t, int V) { return (uint32_t)t < (u
 // 256 / lanes groups of `lanes` threads, each R rows at a time: their tokens,
 // then their elements, are loaded together.  16,384 rows of 2,048 bf16: 17 us,
 // 67 MB written; hot words' rows come from the caches.
-template <typename T, int N, int R>
+template <typename T, int R>
 __global__ __launch_bounds__(256) void embed_lookup_kernel(EmbedLookupArgs a, int lanes) {
+    constexpr int N = Pack<T>::kElems;
     const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     const int64_t i0 = ((int64_t)blockIdx.x * (256 / lanes) + group) * R;
     int t[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) t[r] = i0 + r < a.n ? a.tokens[i0 + r] : -1;
     for (int d = (blockIdx.y * lanes + lane) * N; d < a.D; d += gridDim.y * lanes * N) {
-        typename Pack<T, N>::Raw x[R];
+        typename Pack<T>::Raw x[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (in_table(t[r], a.V)) x[r] = Pack<T, N>::raw((const T*)a.weight + (int64_t)t[r] * a.wstride + d);
+            if (in_table(t[r], a.V)) x[r] = Pack<T>::raw((const T*)a.weight + (int64_t)t[r] * a.wstride + d, a.D - d);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (i0 + r >= a.n) break;
             float y[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) y[e] = in_table(t[r], a.V) ? Pack<T, N>::value(x[r], e) * a.scale : 0.0f;
-            Pack<T, N>::store((T*)a.out + (i0 + r) * a.ostride + d, y);
+            for (int e = 0; e < N; ++e) y[e] = in_table(t[r], a.V) ? Pack<T>::value(x[r], e) * a.scale : 0.0f;
+            Pack<T>::store((T*)a.out + (i0 + r) * a.ostride + d, a.D - d, y);
         }
     }
 }
@@ -117,8 +142,9 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(EmbedLookupArgs a, in
 // A workgroup owns the words [x*words, (x+1)*words).  It lists the positions of
 // its words' tokens in order, ranks them by word (counting the better ones in
 // LDS: the list is short), and its groups of threads take the words in turn.
-template <typename T, int N>
+template <typename T>
 __global__ __launch_bounds__(256) void embed_few_kernel(EmbedBackwardArgs a, int lanes, int words) {
+    constexpr int N = Pack<T>::kElems;
     __shared__ int pos[kEmbedFew], word[kEmbedFew], sorted[kEmbedFew], wcount[4];
     __shared__ int first[kFewWords], count[kFewWords];
     const int v0 = blockIdx.x * words, nv = min(words, a.V - v0);
@@ -160,8 +186,8 @@ __global__ __launch_bounds__(256) void embed_few_kernel(EmbedBackwardArgs a, int
         for (int d = lane * N; d < a.D; d += lanes * N) {
             float s[N] = {};
 #pragma unroll 4
-            for (int q = 0; q < c; ++q) add_row<T, N>(a, sorted[f + q], d, s);
-            put_word<T, N>(a, v0 + v, d, s);
+            for (int q = 0; q < c; ++q) add_row<T>(a, sorted[f + q], d, s);
+            put_word<T>(a, v0 + v, d, s);
         }
     }
 }
@@ -188,22 +214,22 @@ struct Fill {
     int first;      // fill workgroup of this launch's first
     int64_t rows;   // of a fill workgroup
     int32_t size;   // bytes of an element
-    int32_t wide;   // rows of whole 16-byte chunks
 };
 
 __device__ void fill_zeros(const EmbedBackwardArgs& a, const Fill& f, int wg) {
     const int64_t r0 = (int64_t)(f.first + wg) * f.rows, r1 = min((int64_t)a.V, r0 + f.rows);
-    if (f.wide && a.wstride == a.D) {  // one run
-        u32x4* o = (u32x4*)((char*)a.gweight + r0 * a.D * f.size);
-        const int64_t n = (r1 - r0) * a.D * f.size / 16;
-        for (int64_t i = threadIdx.x; i < n; i += blockDim.x) o[i] = u32x4{0, 0, 0, 0};
+    typedef u32x4 Anywhere __attribute__((aligned(2)));
+    const auto zeros = [&](char* o, int64_t bytes) {
+        for (int64_t i = (int64_t)threadIdx.x * 16; i + 16 <= bytes; i += blockDim.x * 16) *(Anywhere*)(o + i) = u32x4{0, 0, 0, 0};
+        const int64_t end = bytes / 16 * 16 + (int64_t)threadIdx.x * 2;  // elements are of two bytes or four
+        if (end < bytes) *(uint16_t*)(o + end) = 0;
+    };
+    char* o = (char*)a.gweight + r0 * a.wstride * f.size;
+    if (a.wstride == a.D) {  // one run
+        zeros(o, (r1 - r0) * a.D * f.size);
         return;
     }
-    for (int64_t r = r0; r < r1; ++r)
-        for (int d = threadIdx.x; d < a.D; d += blockDim.x) {
-            if (f.size == 2) ((uint16_t*)a.gweight)[r * a.wstride + d] = 0;
-            else ((uint32_t*)a.gweight)[r * a.wstride + d] = 0;
-        }
+    for (int64_t r = r0; r < r1; ++r, o += a.wstride * f.size) zeros(o, (int64_t)a.D * f.size);
 }
 
 __global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedBackwardArgs a, const int32_t* keys, int nb, int shift,
@@ -338,9 +364,10 @@ __global__ __launch_bounds__(kSortThreads) void embed_move_kernel(EmbedBackwardA
 // part 1 (to part 0 if it did both).
 // Whole: a group is whole waves, so its words are the same in every lane of a
 // wave and the branches on them are scalar.
-template <typename T, int N, bool Whole>
+template <typename T, bool Whole>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, const int32_t* __restrict__ keys,
                                                         const int32_t* __restrict__ pos, int lanes, int tile, int tiles) {
+    constexpr int N = Pack<T>::kElems;
     const auto uniform = [](int x) { return Whole ? __builtin_amdgcn_readfirstlane(x) : x; };
     const int g = uniform(blockIdx.x * (256 / lanes) + threadIdx.x / lanes), lane = threadIdx.x % lanes;
     if (g >= tiles) return;
@@ -356,7 +383,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
 #pragma unroll
                 for (int e = 0; e < N; ++e) p[e] = s[e];
             } else {
-                put_word<T, N>(a, v, d, s);
+                put_word<T>(a, v, d, s);
             }
 #pragma unroll
             for (int e = 0; e < N; ++e) s[e] = 0.0f;
@@ -369,12 +396,12 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
             pn[u] = i0 + u < i1 ? pos[i0 + u] : 0;
         }
         for (int i = i0; i < i1 && v < a.V; i += kAhead) {
-            typename Pack<T, N>::Raw x[kAhead];
+            typename Pack<T>::Raw x[kAhead];
             int k[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 k[u] = uniform(kn[u]);
-                if (k[u] < a.V) x[u] = Pack<T, N>::raw((const T*)a.grad + (int64_t)uniform(pn[u]) * a.gstride + d);
+                if (k[u] < a.V) x[u] = Pack<T>::raw((const T*)a.grad + (int64_t)uniform(pn[u]) * a.gstride + d, a.D - d);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -388,7 +415,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
                 v = k[u];
                 if (v < a.V) {
 #pragma unroll
-                    for (int e = 0; e < N; ++e) s[e] += Pack<T, N>::value(x[u], e);
+                    for (int e = 0; e < N; ++e) s[e] += Pack<T>::value(x[u], e);
                 }
             }
         }
@@ -401,9 +428,10 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedBackwardArgs a, con
 // parts in order, and the runs' sums are added in order.
 constexpr int kJoinThreads = 512;
 
-template <typename T, int N>
+template <typename T>
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedBackwardArgs a, const int32_t* keys, int lanes, int tile,
                                                                   int tiles) {
+    constexpr int N = Pack<T>::kElems;
     __shared__ float runs[kJoinThreads * N];
     const int g = blockIdx.x;
     const int i0 = g * tile, i1 = i0 + tile;
@@ -443,18 +471,12 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedBackwardA
             for (int r = 1; r < groups; ++r)
 #pragma unroll
                 for (int e = 0; e < N; ++e) s[e] += runs[e * kJoinThreads + r * lanes + lane];
-            put_word<T, N>(a, v, d, s);
+            put_word<T>(a, v, d, s);
         }
     }
 }
 
 // ------------------------------------------------------------------ host
-
-template <typename T>
-bool rows_wide(const void* p, int64_t stride, int D) {
-    const int n = 16 / (int)sizeof(T);
-    return (uintptr_t)p % 16 == 0 && stride % n == 0 && D % n == 0;
-}
 
 // Threads to a row of `chunks` loads: a power of two, at most 256.
 int lanes_for(int chunks) {
@@ -463,32 +485,34 @@ int lanes_for(int chunks) {
     return l;
 }
 
-template <typename T, int N>
+template <typename T>
 hipError_t lookup_t(const EmbedLookupArgs& a, hipStream_t st) {
+    constexpr int N = Pack<T>::kElems;
     const int lanes = lanes_for((a.D + N - 1) / N), groups = 256 / lanes;
     // four rows a group once that still leaves several workgroups to a CU
     const int per = a.n >= 4 * 2048 * groups ? 4 : 1;
     const dim3 grid((unsigned)((a.n + (int64_t)groups * per - 1) / (groups * per)));
-    if (per == 4) embed_lookup_kernel<T, N, 4><<<grid, 256, 0, st>>>(a, lanes);
-    else embed_lookup_kernel<T, N, 1><<<grid, 256, 0, st>>>(a, lanes);
+    if (per == 4) embed_lookup_kernel<T, 4><<<grid, 256, 0, st>>>(a, lanes);
+    else embed_lookup_kernel<T, 1><<<grid, 256, 0, st>>>(a, lanes);
     return hipGetLastError();
 }
 
-template <typename T, int N>
+template <typename T>
 hipError_t backward_t(const EmbedBackwardArgs& a, hipStream_t st) {
+    constexpr int N = Pack<T>::kElems;
     const int chunks = (a.D + N - 1) / N;
     const int lanes = lanes_for(chunks), groups = 256 / lanes;
     if (a.n <= kEmbedFew) {
         // about 32 KB of the gradient to a workgroup
         int words = (int)((32 << 10) / ((int64_t)a.D * sizeof(T)));
         words = words < groups ? groups : (words < kFewWords ? words : kFewWords);
-        embed_few_kernel<T, N><<<dim3((unsigned)((a.V + words - 1) / words)), 256, 0, st>>>(a, lanes, words);
+        embed_few_kernel<T><<<dim3((unsigned)((a.V + words - 1) / words)), 256, 0, st>>>(a, lanes, words);
         return hipGetLastError();
     }
     const EmbedPlan p = embed_plan(a.n, a.V, lanes);
     // fill workgroups of about 128 KB, spread over the sort's launches
     const int64_t row_bytes = (int64_t)a.D * sizeof(T);
-    Fill f{0, ((128 << 10) + row_bytes - 1) / row_bytes, (int32_t)sizeof(T), N > 1};
+    Fill f{0, ((128 << 10) + row_bytes - 1) / row_bytes, (int32_t)sizeof(T)};
     const int fills = a.accumulate ? 0 : (int)((a.V + f.rows - 1) / f.rows);
     int launch = 0;
     const auto share = [&]() {  // sets f.first, returns the launch's fill workgroups
@@ -510,9 +534,9 @@ hipError_t backward_t(const EmbedBackwardArgs& a, hipStream_t st) {
         pos = a.ws.pos[out];
     }
     const dim3 grid((unsigned)((p.tiles + groups - 1) / groups));
-    if (lanes >= 64) embed_sum_kernel<T, N, true><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
-    else embed_sum_kernel<T, N, false><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
-    embed_join_kernel<T, N><<<dim3((unsigned)p.tiles), kJoinThreads, 0, st>>>(a, keys, lanes, p.tile, p.tiles);
+    if (lanes >= 64) embed_sum_kernel<T, true><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
+    else embed_sum_kernel<T, false><<<grid, 256, 0, st>>>(a, keys, pos, lanes, p.tile, p.tiles);
+    embed_join_kernel<T><<<dim3((unsigned)p.tiles), kJoinThreads, 0, st>>>(a, keys, lanes, p.tile, p.tiles);
     return hipGetLastError();
 }
 
@@ -535,20 +559,12 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int lanes) {
 
 hipError_t launch_embed_lookup(const EmbedLookupArgs& a, int dtype, hipStream_t st) {
     if (a.n == 0) return hipSuccess;
-    if (dtype == GR_BF16)
-        return rows_wide<uint16_t>(a.weight, a.wstride, a.D) && rows_wide<uint16_t>(a.out, a.ostride, a.D)
-                   ? lookup_t<uint16_t, 8>(a, st) : lookup_t<uint16_t, 1>(a, st);
-    return rows_wide<float>(a.weight, a.wstride, a.D) && rows_wide<float>(a.out, a.ostride, a.D) ? lookup_t<float, 4>(a, st)
-                                                                                               : lookup_t<float, 1>(a, st);
+    return dtype == GR_BF16 ? lookup_t<uint16_t>(a, st) : lookup_t<float>(a, st);
 }
 
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, int dtype, hipStream_t st) {
     if (a.n == 0 && a.accumulate) return hipSuccess;
-    if (dtype == GR_BF16)
-        return rows_wide<uint16_t>(a.grad, a.gstride, a.D) && rows_wide<uint16_t>(a.gweight, a.wstride, a.D)
-                   ? backward_t<uint16_t, 8>(a, st) : backward_t<uint16_t, 1>(a, st);
-    return rows_wide<float>(a.grad, a.gstride, a.D) && rows_wide<float>(a.gweight, a.wstride, a.D) ? backward_t<float, 4>(a, st)
-                                                                                                 : backward_t<float, 1>(a, st);
+    return dtype == GR_BF16 ? backward_t<uint16_t>(a, st) : backward_t<float>(a, st);
 }
 
 }  // namespace gr

@@ -61,11 +61,14 @@ __device__ __forceinline__ bool has_target(const HeadArgs& a, int n) {
 
 // ------------------------------------------------------------ packing
 
-// Elements [d, d + 8) of a row: 16-byte loads where `wide` (the row starts on 16
-// bytes), zeros behind D.
-__device__ __forceinline__ void load8(const float* src, int d, int D, bool wide, float (&x)[8]) {
-    if (wide && d + 8 <= D) {
-        const f32x4v lo = *(const f32x4v*)(src + d), hi = *(const f32x4v*)(src + d + 4);
+// Elements [d, d + 8) of a row, zeros behind D.  Rows need no alignment beyond
+// the element's: the hardware takes 16-byte loads anywhere.
+typedef f32x4v f32x4_anywhere __attribute__((aligned(4)));
+typedef u32x4 u32x4_anywhere __attribute__((aligned(2)));
+
+__device__ __forceinline__ void load8(const float* src, int d, int D, float (&x)[8]) {
+    if (d + 8 <= D) {
+        const f32x4v lo = *(const f32x4_anywhere*)(src + d), hi = *(const f32x4_anywhere*)(src + d + 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = lo[e], x[e + 4] = hi[e];
         return;
@@ -73,8 +76,8 @@ __device__ __forceinline__ void load8(const float* src, int d, int D, bool wide,
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = d + e < D ? src[d + e] : 0.0f;
 }
-__device__ __forceinline__ u32x4 load8_bits(const uint16_t* src, int d, int D, bool wide) {
-    if (wide && d + 8 <= D) return *(const u32x4*)(src + d);
+__device__ __forceinline__ u32x4 load8_bits(const uint16_t* src, int d, int D) {
+    if (d + 8 <= D) return *(const u32x4_anywhere*)(src + d);
     u32x4 v = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -83,15 +86,13 @@ __device__ __forceinline__ u32x4 load8_bits(const uint16_t* src, int d, int D, b
 }
 
 // Row `src` of D elements into planes of Dp (a multiple of 8).
-__device__ __forceinline__ void pack_row(const uint16_t* src, int D, int Dp, bool wide, uint16_t* dst, int64_t, int lane,
-                                         int lanes) {
-    for (int d = lane * 8; d < Dp; d += lanes * 8) *(u32x4*)(dst + d) = load8_bits(src, d, D, wide);
+__device__ __forceinline__ void pack_row(const uint16_t* src, int D, int Dp, uint16_t* dst, int64_t, int lane, int lanes) {
+    for (int d = lane * 8; d < Dp; d += lanes * 8) *(u32x4*)(dst + d) = load8_bits(src, d, D);
 }
-__device__ __forceinline__ void pack_row(const float* src, int D, int Dp, bool wide, uint16_t* dst, int64_t plane, int lane,
-                                         int lanes) {
+__device__ __forceinline__ void pack_row(const float* src, int D, int Dp, uint16_t* dst, int64_t plane, int lane, int lanes) {
     for (int d = lane * 8; d < Dp; d += lanes * 8) {
         float x[8];
-        load8(src, d, D, wide, x);
+        load8(src, d, D, x);
         u32x4 v[3];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -107,12 +108,12 @@ __device__ __forceinline__ void pack_row(const float* src, int D, int Dp, bool w
 
 // Row `src` scaled by a power of two into two fp16 planes (gemm_tile.h), by one
 // wave; returns what divides the scale out again.
-__device__ __forceinline__ float pack_row_half(const float* src, int D, int Dp, bool wide, uint16_t* dst, int64_t plane, int lane) {
+__device__ __forceinline__ float pack_row_half(const float* src, int D, int Dp, uint16_t* dst, int64_t plane, int lane) {
     typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
     float most = 0.0f;
     for (int d = lane * 8; d < Dp; d += 512) {
         float x[8];
-        load8(src, d, D, wide, x);
+        load8(src, d, D, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
     }
@@ -122,7 +123,7 @@ __device__ __forceinline__ float pack_row_half(const float* src, int D, int Dp, 
     const float scale = __uint_as_float((uint32_t)(127 + up) << 23);
     for (int d = lane * 8; d < Dp; d += 512) {
         float x[8];
-        load8(src, d, D, wide, x);
+        load8(src, d, D, x);
         u32x4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -136,12 +137,6 @@ __device__ __forceinline__ float pack_row_half(const float* src, int D, int Dp, 
         *(u32x4*)(dst + plane + d) = lo;
     }
     return __uint_as_float((uint32_t)(127 - up) << 23);
-}
-
-// Rows from `p` on, `stride` apart, all start on 16 bytes.
-template <typename T>
-__device__ __forceinline__ bool rows_wide(const T* p, int64_t stride) {
-    return (uintptr_t)p % 16 == 0 && stride % (16 / (int)sizeof(T)) == 0;
 }
 
 // what a packing kernel writes: planes as they are (bf16: one, fp32: three, for
@@ -175,7 +170,6 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
     __syncthreads();
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int r2 = min(r0 + rows_per_wg, a.N);
-    const bool wide = rows_wide((const T*)a.hidden, a.hstride);
     int before = base;
     for (int r1 = r0; r1 < r2; r1 += 64) {
         const int mine = r1 + lane;
@@ -198,10 +192,10 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(HeadArgs a, int64_t rows
             if ((k & 3) != wave) continue;
             const T* src = (const T*)a.hidden + (int64_t)(r1 + __builtin_ctzll(rest)) * a.hstride;
             const int64_t at = (int64_t)(before + k) * a.plan.Dp, plane = rows_cap * a.plan.Dp;
-            if (what & kPackPlanes) pack_row(src, a.D, a.plan.Dp, wide, a.ws.H + at, plane, lane, 64);
+            if (what & kPackPlanes) pack_row(src, a.D, a.plan.Dp, a.ws.H + at, plane, lane, 64);
             if constexpr (sizeof(T) == 4) {
                 if (what & kPackHalves) {
-                    const float f = pack_row_half(src, a.D, a.plan.Dp, wide, a.ws.Hh + at, plane, lane);
+                    const float f = pack_row_half(src, a.D, a.plan.Dp, a.ws.Hh + at, plane, lane);
                     if (lane == 0) a.ws.hdown[before + k] = f;
                 }
             }
@@ -226,12 +220,11 @@ __global__ __launch_bounds__(256) void pack_words_kernel(HeadArgs a, int v0, int
     const int v = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (v >= nv) return;
     const T* src = (const T*)a.weight + (int64_t)(v0 + v) * a.wstride;
-    const bool wide = rows_wide((const T*)a.weight, a.wstride);
     const int64_t at = (int64_t)v * a.plan.Dp, plane = (int64_t)a.plan.Vw * a.plan.Dp;
-    if (what & kPackPlanes) pack_row(src, a.D, a.plan.Dp, wide, a.ws.W + at, plane, lane, 64);
+    if (what & kPackPlanes) pack_row(src, a.D, a.plan.Dp, a.ws.W + at, plane, lane, 64);
     if constexpr (sizeof(T) == 4) {
         if (what & kPackHalves) {
-            const float f = pack_row_half(src, a.D, a.plan.Dp, wide, a.ws.Wh + at, plane, lane);
+            const float f = pack_row_half(src, a.D, a.plan.Dp, a.ws.Wh + at, plane, lane);
             if (lane == 0) a.ws.wdown[v] = f;
         }
     }
@@ -453,14 +446,14 @@ struct Raw8;  // eight elements as loaded
 template <>
 struct Raw8<uint16_t> {
     u32x4 v;
-    __device__ __forceinline__ void load(const uint16_t* p, int d, int D, bool wide) { v = load8_bits(p, d, D, wide); }
+    __device__ __forceinline__ void load(const uint16_t* p, int d, int D) { v = load8_bits(p, d, D); }
     __device__ __forceinline__ void zero() { v = u32x4{0, 0, 0, 0}; }
     __device__ __forceinline__ void planes(bf16x8 (&b)[1]) const { b[0] = __builtin_bit_cast(bf16x8, v); }
 };
 template <>
 struct Raw8<float> {
     float x[8];
-    __device__ __forceinline__ void load(const float* p, int d, int D, bool wide) { load8(p, d, D, wide, x); }
+    __device__ __forceinline__ void load(const float* p, int d, int D) { load8(p, d, D, x); }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = 0.0f;
@@ -488,7 +481,6 @@ __global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) 
     __shared__ __align__(16) uint16_t hs[2][PL][kRows][StepK];
     __shared__ float sm[MaxWaves][kRows], ss[MaxWaves][kRows], szt[kRows];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const bool hwide = rows_wide((const T*)a.hidden, a.hstride), wwide = rows_wide((const T*)a.weight, a.wstride);
     const int v0 = (blockIdx.x * waves + wave) * 16;
     const int steps = tiles_of(a.D, StepK);
     // the width is walked in a circle from another step in every workgroup: rows
@@ -512,7 +504,7 @@ __global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) 
 #pragma unroll
         for (int q = 0; q < kItems; ++q) {
             const int d = c * StepK + (threadIdx.x % kChunks) * 8;
-            if (hok[q] && d < a.D) hr[q].load(hrow[q], d, a.D, hwide);
+            if (hok[q] && d < a.D) hr[q].load(hrow[q], d, a.D);
             else hr[q].zero();
         }
     };
@@ -538,7 +530,7 @@ __global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) 
 #pragma unroll
         for (int kk = 0; kk < kParts32; ++kk) {
             const int d = c * StepK + kk * 32 + (lane >> 4) * 8;
-            if (d < a.D) w.r[kk].load(wrow, d, a.D, wwide);
+            if (d < a.D) w.r[kk].load(wrow, d, a.D);
             else w.r[kk].zero();
         }
     };
@@ -686,36 +678,32 @@ __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand
 
 // ------------------------------------------------------------- gradients
 
-// Four elements of a row of an output: 8 or 16 bytes at once where `wide` (the
-// rows start on as many); `add`: to what it holds; only `left` of them exist.
-__device__ __forceinline__ void put4(float* o, int left, bool wide, bool add, f32x4v x) {
-    if (wide && left >= 4) {
-        if (add) x += *(const f32x4v*)o;
-        *(f32x4v*)o = x;
+// Four elements of a row of an output, 8 or 16 bytes at once; `add`: to what it
+// holds; only `left` of them exist.
+__device__ __forceinline__ void put4(float* o, int left, bool add, f32x4v x) {
+    if (left >= 4) {
+        if (add) x += *(const f32x4_anywhere*)o;
+        *(f32x4_anywhere*)o = x;
         return;
     }
     for (int r = 0; r < 4; ++r)
         if (r < left) o[r] = add ? o[r] + x[r] : x[r];
 }
-__device__ __forceinline__ void put4(uint16_t* o, int left, bool wide, bool add, f32x4v x) {
+__device__ __forceinline__ void put4(uint16_t* o, int left, bool add, f32x4v x) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    if (wide && left >= 4) {
+    typedef u32x2 Anywhere __attribute__((aligned(2)));
+    if (left >= 4) {
         if (add) {
-            const u32x2 old = *(const u32x2*)o;
+            const u32x2 old = *(const Anywhere*)o;
             x += f32x4v{__uint_as_float(old[0] << 16), __uint_as_float(old[0] & 0xFFFF0000u), __uint_as_float(old[1] << 16),
                         __uint_as_float(old[1] & 0xFFFF0000u)};
         }
-        *(u32x2*)o = u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
+        *(Anywhere*)o = u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
         return;
     }
     for (int r = 0; r < 4; ++r)
         if (r < left) o[r] = bf16_bits(add ? bf16_value(o[r]) + x[r] : x[r]);
 }
-template <typename T>
-__device__ __forceinline__ bool rows_wide4(const T* p, int64_t stride) {
-    return (uintptr_t)p % (4 * sizeof(T)) == 0 && stride % 4 == 0;
-}
-
 // Split s of the piece's words: its share of grad_hidden, added to what the
 // pieces before left.  out: the last piece of an unsplit product writes the
 // rows themselves (an own pass over the fp32 sums took 33 us more for 40,960
@@ -741,7 +729,6 @@ __global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Oper
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
     float* gh = a.ws.gh + (int64_t)s * a.N * a.plan.Dp;
-    const bool wide = out && rows_wide4((const T*)a.ghidden, a.ghstride);
 #pragma unroll
     for (int j = 0; j < Tile::FN; ++j) {
         const int n = rn + j * 16 + (lane & 15);
@@ -753,7 +740,7 @@ __global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Oper
             if (d >= a.plan.Dp) continue;
             f32x4v* o = (f32x4v*)(gh + (int64_t)n * a.plan.Dp + d);
             const f32x4v x = first ? acc[i][j] : *o + acc[i][j];
-            if (out) put4(row + d, a.D - d, wide, false, x);
+            if (out) put4(row + d, a.D - d, false, x);
             else *o = x;
         }
     }
@@ -766,12 +753,12 @@ __global__ __launch_bounds__(256) void head_ghidden_out_kernel(HeadArgs a, int s
     const int n = blockIdx.x;
     const int at = a.ws.place[n];
     const int64_t stride = (int64_t)a.N * a.plan.Dp;
-    const bool wide = rows_wide4((const T*)a.ghidden, a.ghstride);
     for (int d = threadIdx.x * 4; d < a.D; d += 1024) {
         f32x4v s = {};
         if (at >= 0)
+#pragma unroll 8
             for (int q = 0; q < splits; ++q) s += *(const f32x4v*)(a.ws.gh + q * stride + (int64_t)at * a.plan.Dp + d);
-        put4((T*)a.ghidden + (int64_t)n * a.ghstride + d, a.D - d, wide, false, s);
+        put4((T*)a.ghidden + (int64_t)n * a.ghstride + d, a.D - d, false, s);
     }
 }
 
@@ -792,7 +779,6 @@ __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int6
     const int k0 = s * per, k1 = min(count, k0 + per);
     f32x4v acc[Tile::FM][Tile::FN] = {};
     Tile::run(hidden_operand(a, rows_cap, count), m0, grad_operand(a, rows_cap, count), n0, k0, k1, lds, acc);
-    const bool wide = rows_wide4((const T*)a.gweight, a.gwstride);
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int rm = m0 + (wave / (Tile::BN / Tile::WN)) * Tile::WM, rn = n0 + (wave % (Tile::BN / Tile::WN)) * Tile::WN;
@@ -805,7 +791,7 @@ __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int6
             const int d = rm + i * 16 + (lane >> 4) * 4;
             if (d >= a.plan.Dp) continue;
             if (splits > 1) *(f32x4v*)(a.ws.gw + ((int64_t)s * nv + v) * a.plan.Dp + d) = acc[i][j];
-            else put4((T*)a.gweight + (int64_t)(vp + v) * a.gwstride + d, a.D - d, wide, a.accumulate, acc[i][j]);
+            else put4((T*)a.gweight + (int64_t)(vp + v) * a.gwstride + d, a.D - d, a.accumulate, acc[i][j]);
         }
     }
 }
@@ -813,11 +799,11 @@ __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int6
 template <typename T>
 __global__ __launch_bounds__(256) void head_gweight_out_kernel(HeadArgs a, int vp, int nv, int splits) {
     const int v = blockIdx.x;
-    const bool wide = rows_wide4((const T*)a.gweight, a.gwstride);
     for (int d = threadIdx.x * 4; d < a.D; d += 1024) {
         f32x4v s = {};
+#pragma unroll 8
         for (int q = 0; q < splits; ++q) s += *(const f32x4v*)(a.ws.gw + ((int64_t)q * nv + v) * a.plan.Dp + d);
-        put4((T*)a.gweight + (int64_t)(vp + v) * a.gwstride + d, a.D - d, wide, a.accumulate, s);
+        put4((T*)a.gweight + (int64_t)(vp + v) * a.gwstride + d, a.D - d, a.accumulate, s);
     }
 }
 
@@ -837,11 +823,13 @@ __global__ __launch_bounds__(256) void head_zero_kernel(HeadArgs a) {
 // consecutive elements: both operands agree on which.
 constexpr int kSmallMost = 512;  // rows and words at most: their share of G is 33 KB of LDS
 
-__device__ __forceinline__ f32x4v load4_wide(const float* p) { return *(const f32x4v*)p; }
-__device__ __forceinline__ f32x4v load4_wide(const uint16_t* p) {
-    const uint2 v = *(const uint2*)p;
-    return f32x4v{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                  __uint_as_float(v.y & 0xFFFF0000u)};
+__device__ __forceinline__ f32x4v load4(const float* p) { return *(const f32x4_anywhere*)p; }
+__device__ __forceinline__ f32x4v load4(const uint16_t* p) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef u32x2 Anywhere __attribute__((aligned(2)));
+    const u32x2 v = *(const Anywhere*)p;
+    return f32x4v{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u), __uint_as_float(v[1] << 16),
+                  __uint_as_float(v[1] & 0xFFFF0000u)};
 }
 
 template <typename T>
@@ -853,7 +841,6 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
     const int r0 = rows ? blockIdx.x * 16 : 0, w0 = rows ? 0 : (blockIdx.x - row_wgs) * 16;
     const int others = rows ? a.V : a.N;  // the length of the second product
     const int pitch = (others + 15) / 16 * 16 + 4;
-    const bool hwide = rows_wide4((const T*)a.hidden, a.hstride), wwide = rows_wide4((const T*)a.weight, a.wstride);
 
     // Loads are from clamped places and unconditional (a branch around each would
     // leave one in flight); what does not exist is zeroed behind them.
@@ -866,14 +853,12 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
         const int t = nin ? a.targets[n] - (v - li) : -1;
         f32x4v acc = {};
         int d0 = 0;
-        if (hwide && wwide) {
 #pragma unroll 4
-            for (; d0 + 16 <= a.D; d0 += 16) {
-                const f32x4v x = load4_wide(wp + d0 + lk * 4), y = load4_wide(hp + d0 + lk * 4);
+        for (; d0 + 16 <= a.D; d0 += 16) {
+            const f32x4v x = load4(wp + d0 + lk * 4), y = load4(hp + d0 + lk * 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin ? x[e] : 0.0f, nin ? y[e] : 0.0f, acc, 0, 0, 0);
-            }
+            for (int e = 0; e < 4; ++e)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin ? x[e] : 0.0f, nin ? y[e] : 0.0f, acc, 0, 0, 0);
         }
         for (; d0 < a.D; d0 += 16) {
 #pragma unroll
@@ -901,7 +886,6 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
     const bool stored = mine < (rows ? a.N : a.V);
     const bool zero = rows && !has_target(a, mine);
     T* out = rows ? (T*)a.ghidden + (int64_t)mine * a.ghstride : (T*)a.gweight + (int64_t)mine * a.gwstride;
-    const bool owide = rows ? rows_wide4((const T*)a.ghidden, a.ghstride) : rows_wide4((const T*)a.gweight, a.gwstride);
     const T* left = rows ? (const T*)a.weight : (const T*)a.hidden;
     const int64_t lstride = rows ? a.wstride : a.hstride;
     const int padded = (others + 15) / 16 * 16;
@@ -918,7 +902,7 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
             }
         }
         const int od = d0 + lk * 4;
-        if (stored && od < a.D) put4(out + od, a.D - od, owide, !rows && a.accumulate, zero ? f32x4v{} : acc);
+        if (stored && od < a.D) put4(out + od, a.D - od, !rows && a.accumulate, zero ? f32x4v{} : acc);
     }
 }
 
