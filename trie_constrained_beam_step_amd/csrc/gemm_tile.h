@@ -82,10 +82,12 @@ __device__ __forceinline__ f32x4v mfma16(bf16x8 a, bf16x8 b, f32x4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// BM x BN tile, waves of WM x WN, BK deep (32 or 64), PL planes (Half: of fp16).
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int PL_, bool AAcross, bool BAcross, bool Half_ = false>
+// BM x BN tile, waves of WM x WN, BK deep (32 or 64), PL planes (Half: of fp16),
+// ST stages of LDS.
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int PL_, bool AAcross, bool BAcross, bool Half_ = false, int ST_ = 2>
 struct GemmTile {
     static constexpr bool Half = Half_;
+    static constexpr int ST = ST_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, PL = PL_;
     static constexpr int NT = (BM / WM) * (BN / WN) * 64;
     static constexpr int FM = WM / 16, FN = WN / 16;
@@ -94,9 +96,11 @@ struct GemmTile {
     // 16,384 x 7,424 (grad_weight's) 1,235 TFLOP/s against 1,094 in step, at
     // 32,768 x 7,424 x 2,048 (the logits', both "along") 1,160 against 1,253.
     static constexpr bool kTurns = AAcross && NT == 512;
+    static_assert(!kTurns || ST == 2, "turns take two stages");
     static constexpr bool kPerm = !AAcross;  // rows of A are interleaved (frag_row)
     static constexpr int ABytes = BM * BK * 2, BBytes = BN * BK * 2;  // a plane's
     static constexpr int Stage = PL * (ABytes + BBytes);
+    static constexpr int Lds = ST * Stage;
 
     // Copies one operand's R x BK tile (all planes) into LDS, one k step after
     // the other.
@@ -217,7 +221,7 @@ struct GemmTile {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    // acc += the tile at rows m0 of A and n0 of B, k in [k0, k1).  lds: two
+    // acc += the tile at rows m0 of A and n0 of B, k in [k0, k1).  lds: the
     // stages.  k0 is a multiple of 8 and k1 of BK, or what lies behind k1 is
     // zero in one operand and finite in the other (rows behind an "across"
     // operand's end are zero).
@@ -230,24 +234,40 @@ struct GemmTile {
         char* wave_lds = lds + wave * 1024;
         const int steps = (k1 - k0 + BK - 1) / BK;
         const auto load = [&](int i) {
-            char* to = wave_lds + (i & 1) * Stage;
+            char* to = wave_lds + i % ST * Stage;
             fa(to, k1 - k0 - i * BK);
             fb(to + PL * ABytes, k1 - k0 - i * BK);
         };
-        load(0);
-        if (kTurns) turns(lds, steps, wave >= NT / 128, load, acc);
-        else together(lds, steps, load, acc);
+        if (kTurns) {
+            load(0);
+            turns(lds, steps, wave >= NT / 128, load, acc);
+        } else {
+            together(lds, steps, load, acc);
+        }
     }
 
-    // All waves in step: the next step's loads are issued at the start of a
-    // step, whose matrix instructions hide them.
+    // All waves in step: ST - 1 steps are in flight before the first, and each
+    // issues the loads of the one ST - 1 behind it at its start, into the stage
+    // that the step before it has read.  Its own loads are the oldest but those
+    // of ST - 2 steps.
     template <typename Load>
     static __device__ __forceinline__ void together(const char* lds, int steps, const Load& load, f32x4v (&acc)[FM][FN]) {
+        constexpr int kYounger = (ST - 2) * PL * (ABytes + BBytes) / (NT * 16);  // loads of a wave
+        static_assert(kYounger < 64, "the wait counts up to 63");
+        for (int i = 0; i < ST - 1; ++i)
+            if (i < steps) load(i);
         for (int i = 0; i < steps; ++i) {
-            stage_barrier(true);
-            if (i + 1 < steps) load(i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" ::: "memory");
+            // vmcnt(kYounger), or (0) where fewer steps are in flight; lgkmcnt(0)
+            if (i + ST - 2 < steps) __builtin_amdgcn_s_waitcnt((kYounger & 15) | (kYounger >> 4) << 14 | 0x0070);
+            else __builtin_amdgcn_s_waitcnt(0x0070);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + ST - 1 < steps) load(i + ST - 1);
             __builtin_amdgcn_s_setprio(1);
-            multiply(lds + (i & 1) * Stage, acc);
+            multiply(lds + i % ST * Stage, acc);
             __builtin_amdgcn_s_setprio(0);
         }
     }

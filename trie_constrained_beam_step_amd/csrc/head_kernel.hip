@@ -246,39 +246,54 @@ __device__ __forceinline__ void tile_of(int b, int tm, int tn, int& im, int& in)
     in = (id % per) / gm;
 }
 
-// Shapes of the tiles by element type: large ones reuse each operand most,
-// small ones fill the chip where there are few large ones.
-template <typename T, bool AAcross, bool BAcross, bool Large>
+// Shapes of the tiles by element type: large ones reuse each operand most; small
+// ones fill the chip where there are few large ones, two to a CU or, where there
+// is one to a CU at most, with more stages (deep): alone, a workgroup has only
+// its own loads in flight to hide their latency.
+enum Shape { kLarge, kSmall, kDeep };
+
+template <typename T, bool AAcross, bool BAcross, Shape S>
 struct TileFor;
 template <bool AAcross, bool BAcross>
-struct TileFor<uint16_t, AAcross, BAcross, true> {
+struct TileFor<uint16_t, AAcross, BAcross, kLarge> {
     typedef GemmTile<256, 256, 128, 64, 64, 1, AAcross, BAcross> type;
 };
 template <bool AAcross, bool BAcross>
-struct TileFor<uint16_t, AAcross, BAcross, false> {
+struct TileFor<uint16_t, AAcross, BAcross, kSmall> {
     typedef GemmTile<128, 128, 64, 64, 64, 1, AAcross, BAcross> type;
 };
 template <bool AAcross, bool BAcross>
-struct TileFor<float, AAcross, BAcross, true> {
-    typedef GemmTile<256, 128, 64, 64, 32, 3, AAcross, BAcross> type;
+struct TileFor<uint16_t, AAcross, BAcross, kDeep> {
+    typedef GemmTile<128, 128, 64, 64, 64, 1, AAcross, BAcross, false, 4> type;
 };
 template <bool AAcross, bool BAcross>
-struct TileFor<float, AAcross, BAcross, false> {
-    typedef GemmTile<128, 128, 64, 64, 32, 3, AAcross, BAcross> type;
+struct TileFor<float, AAcross, BAcross, kLarge> {
+    typedef GemmTile<256, 128, 64, 64, 32, 3, AAcross, BAcross> type;
 };
+// three planes of a small tile's two stages leave a CU to one workgroup anyway
+template <bool AAcross, bool BAcross>
+struct TileFor<float, AAcross, BAcross, kSmall> {
+    typedef GemmTile<128, 128, 64, 64, 32, 3, AAcross, BAcross, false, 3> type;
+};
+template <bool AAcross, bool BAcross>
+struct TileFor<float, AAcross, BAcross, kDeep> : TileFor<float, AAcross, BAcross, kSmall> {};
 
 // The logits' product: halves where the elements are fp32.
-template <typename T, bool Large>
+template <typename T, Shape S>
 struct LogitTile {
-    typedef typename TileFor<T, false, false, Large>::type type;
+    typedef typename TileFor<T, false, false, S>::type type;
 };
 template <>
-struct LogitTile<float, true> {
+struct LogitTile<float, kLarge> {
     typedef GemmTile<256, 256, 128, 64, 32, 2, false, false, true> type;
 };
 template <>
-struct LogitTile<float, false> {
+struct LogitTile<float, kSmall> {
     typedef GemmTile<128, 128, 64, 64, 32, 2, false, false, true> type;
+};
+template <>
+struct LogitTile<float, kDeep> {
+    typedef GemmTile<128, 128, 64, 64, 32, 2, false, false, true, 4> type;
 };
 
 template <typename Tile>
@@ -323,7 +338,7 @@ __device__ __forceinline__ void unscale_words(const HeadArgs& a, int rm, f32x4v 
 template <typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_parts_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
     static_assert(Tile::WM >= kPartWords, "a part for each wave's words");
-    __shared__ __align__(1024) char lds[2 * Tile::Stage];
+    __shared__ __align__(1024) char lds[Tile::Lds];
     const int count = *a.ws.count;
     int im, in;
     tile_of(blockIdx.x, tiles_of(nv, Tile::BM), tiles_of(a.N, Tile::BN), im, in);
@@ -623,7 +638,7 @@ __global__ __launch_bounds__(MaxWaves * 64) void head_stream_kernel(HeadArgs a) 
 // bf16 case there, 1,150 TFLOP/s, 450 MB of G written.
 template <typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_grad_kernel(HeadArgs a, Operand W, int64_t rows_cap, int vp, int nv) {
-    __shared__ __align__(1024) char lds[2 * Tile::Stage];
+    __shared__ __align__(1024) char lds[Tile::Lds];
     constexpr int PL = Tile::Half ? 3 : Tile::PL;  // of G
     const int count = *a.ws.count;
     int im, in;
@@ -712,7 +727,7 @@ __device__ __forceinline__ void put4(uint16_t* o, int left, bool add, f32x4v x) 
 template <typename T, typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_ghidden_kernel(HeadArgs a, Operand W, int64_t rows_cap, int nv, int splits,
                                                                 bool first, bool out) {
-    __shared__ __align__(1024) char lds[2 * Tile::Stage];
+    __shared__ __align__(1024) char lds[Tile::Lds];
     const int count = *a.ws.count;
     const int tm = tiles_of(a.D, Tile::BM), tn = tiles_of(a.N, Tile::BN);
     const int s = blockIdx.x / (tm * tn);
@@ -768,7 +783,7 @@ __global__ __launch_bounds__(256) void head_ghidden_out_kernel(HeadArgs a, int s
 // piece above, 1,150 TFLOP/s.
 template <typename T, typename Tile>
 __global__ __launch_bounds__(Tile::NT) void head_gweight_kernel(HeadArgs a, int64_t rows_cap, int vp, int nv, int splits) {
-    __shared__ __align__(1024) char lds[2 * Tile::Stage];
+    __shared__ __align__(1024) char lds[Tile::Lds];
     const int count = *a.ws.count;
     const int tm = tiles_of(a.D, Tile::BM), tn = tiles_of(nv, Tile::BN);
     const int s = blockIdx.x / (tm * tn);
@@ -912,49 +927,65 @@ constexpr int kMaxSplits = 64;
 constexpr int kCUs = 256;
 constexpr int kLdsBytes = 160 << 10;  // of a CU
 
-// How a product of m x n with k steps is cut: into large or small tiles, the k
-// axis into splits.  The cost is in k steps of a large tile: rounds of
-// workgroups over the chip, each its k steps and `ends` more for its first
-// loads and its epilogue; small tiles work at four fifths of the large ones'
-// rate, two of them share a CU where their LDS allows.  Splits pay for writing
-// and reading their fp32 sums: a CU moves a large tile's in about six k steps,
-// and the launch that adds them takes about two and a half.  Only splits that fill one, two or three rounds can be the best.
+// How a product of m x n with k steps is cut: into tiles of a shape, the k axis
+// into splits.  The cost is in k steps of a large tile: rounds of workgroups over
+// the chip, each its k steps and `ends` more for its first loads and its
+// epilogue; small tiles work at four fifths of the large ones' rate where two
+// share a CU, at about half of it alone (one wave to a SIMD).  Splits pay
+// for writing and reading their fp32 sums: a CU moves a large tile's in about
+// six k steps, and the launch that adds them takes about two and a half.  Only
+// splits that fill one, two or three rounds can be the best.
 struct Cut {
-    bool large;
+    Shape shape;
     int splits;
     double cost;
 };
 constexpr int kMostRounds = 3;  // of a split product
 
-template <typename Large, typename Small>
-Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split, double ends) {
-    constexpr int kSmallShare = 4 * Small::Stage <= kLdsBytes ? 2 : 1;  // small tiles on a CU
-    constexpr double kSmallStep = (double)kSmallShare * Small::BM * Small::BN / (Large::BM * Large::BN) / 0.8;
-    const int steps = tiles_of(k, Large::BK);
-    Cut best{true, 1, 1e300};
-    for (int large = 1; large >= 0; --large) {
-        const int64_t tiles = large ? (int64_t)tiles_of(m, Large::BM) * tiles_of(n, Large::BN)
-                                    : (int64_t)tiles_of(m, Small::BM) * tiles_of(n, Small::BN);
-        const int slots = large ? kCUs : kSmallShare * kCUs;
-        const double step = large ? 1.0 : kSmallStep;
-        for (int round = 0; round <= (may_split ? kMostRounds : 0); ++round) {
-            int64_t s = 1;
-            if (round > 0) {
-                s = (int64_t)round * slots / tiles;
-                if (s > kMaxSplits) s = kMaxSplits;
-                if (s > steps / 4) s = steps / 4;  // four k steps each, or more
-                if (s < 2) continue;
-            }
-            const double rounds = (double)((tiles * s + slots - 1) / slots);
-            double cost = rounds * ((double)((steps + s - 1) / s) + ends) * step;
-            if (s > 1) cost += 6.0 * step * (double)(tiles * s) / slots + 2.5;
-            if (cost < best.cost * 0.999) best = Cut{large != 0, (int)s, cost};
+template <typename Large, typename Tile>
+void try_cut(Shape shape, int64_t m, int64_t n, int64_t k, bool may_split, double ends, Cut* best) {
+    constexpr int kShare = 2 * Tile::Lds <= kLdsBytes ? 2 : 1;  // workgroups on a CU
+    constexpr double kRate = Tile::BM * Tile::BN == Large::BM * Large::BN ? 1.0 : kShare == 2 ? 0.8 : 0.55;
+    constexpr double kStep = (double)kShare * Tile::BM * Tile::BN * Tile::BK / (Large::BM * Large::BN * Large::BK) / kRate;
+    const int64_t tiles = (int64_t)tiles_of(m, Tile::BM) * tiles_of(n, Tile::BN);
+    const int steps = tiles_of(k, Tile::BK), slots = kShare * kCUs;
+    if (shape == kDeep && tiles > slots) return;  // small tiles then, two to a CU
+    for (int round = 0; round <= (may_split ? kMostRounds : 0); ++round) {
+        int64_t s = 1;
+        if (round > 0) {
+            s = (int64_t)round * slots / tiles;
+            if (s > kMaxSplits) s = kMaxSplits;
+            if (s > steps / 4) s = steps / 4;  // four k steps each, or more
+            if (s < 2) continue;
         }
+        const double rounds = (double)((tiles * s + slots - 1) / slots);
+        double cost = rounds * ((double)((steps + s - 1) / s) + ends) * kStep;
+        if (s > 1) cost += 6.0 * kStep * (double)(tiles * s) / slots + 2.5;
+        if (cost < best->cost * 0.999) *best = Cut{shape, (int)s, cost};
     }
+}
+
+template <typename Large, typename Small, typename Deep>
+Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split, double ends) {
+    Cut best{kLarge, 1, 1e300};
+    try_cut<Large, Large>(kLarge, m, n, k, may_split, ends, &best);
+    try_cut<Large, Small>(kSmall, m, n, k, may_split, ends, &best);
+    try_cut<Large, Deep>(kDeep, m, n, k, may_split, ends, &best);
     return best;
 }
 
-constexpr double kLogitEnds = 7, kSumEnds = 4;  // (cut_product) of the logits and of the gradients
+constexpr double kLogitEnds = 7, kSumEnds = 4;  // of the logits and of the gradients
+
+template <typename T>
+Cut cut_logits(int64_t words, int64_t rows, int64_t dim) {
+    return cut_product<typename LogitTile<T, kLarge>::type, typename LogitTile<T, kSmall>::type, typename LogitTile<T, kDeep>::type>(
+        words, rows, dim, false, kLogitEnds);
+}
+template <typename T, bool BAcross>
+Cut cut_gradient(int64_t m, int64_t n, int64_t k) {
+    return cut_product<typename TileFor<T, true, BAcross, kLarge>::type, typename TileFor<T, true, BAcross, kSmall>::type,
+                       typename TileFor<T, true, BAcross, kDeep>::type>(m, n, k, true, kSumEnds);
+}
 
 constexpr int64_t kPieceElems = 256ll << 20;   // of the logits' gradient at most (512 MB)
 constexpr int64_t kTableElems = 128ll << 20;   // of a packed piece of the table, all planes
@@ -1005,8 +1036,6 @@ void run_parts(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, 
 
 template <typename T>
 hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
-    typedef typename LogitTile<T, true>::type Large;
-    typedef typename LogitTile<T, false>::type Small;
     const int64_t cap = all.plan.part_rows;
     for (int64_t r = 0; r < all.N; r += cap) {
         HeadArgs a = all;
@@ -1044,15 +1073,16 @@ hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
         }
         hipError_t e = pack_rows<T>(a, cap, dtype == GR_BF16 ? kPackPlanes : kPackHalves, false, st);
         if (e != hipSuccess) return e;
-        const bool large = cut_product<Large, Small>(a.V, a.N, a.D, false, kLogitEnds).large;
+        const Shape shape = cut_logits<T>(a.V, a.N, a.D).shape;
         const int step = reads_in_place(a.weight, a.wstride, a.D, dtype) ? a.V : a.plan.Vw;
         for (int v = 0; v < a.V; v += step) {
             const int nv = a.V - v < step ? a.V - v : step;
             const Operand W = words_operands<T>(a, v, nv, false, dtype, st).logits;
-            if (large) run_parts<Large>(a, W, cap, v, nv, st);
-            else run_parts<Small>(a, W, cap, v, nv, st);
+            if (shape == kLarge) run_parts<typename LogitTile<T, kLarge>::type>(a, W, cap, v, nv, st);
+            else if (shape == kSmall) run_parts<typename LogitTile<T, kSmall>::type>(a, W, cap, v, nv, st);
+            else run_parts<typename LogitTile<T, kDeep>::type>(a, W, cap, v, nv, st);
         }
-        const int parts = tiles_of(a.V, large ? Large::WM : Small::WM);
+        const int parts = tiles_of(a.V, shape == kLarge ? LogitTile<T, kLarge>::type::WM : LogitTile<T, kSmall>::type::WM);
         int rb = 256;  // four threads to a row, more where it has many parts
         while (rb > 16 && parts > 8 * (1024 / rb)) rb /= 2;
         head_join_kernel<<<dim3((unsigned)tiles_of(a.N, rb)), 1024, 0, st>>>(a, cap, parts, rb, true);
@@ -1094,15 +1124,8 @@ bool small_backward(const HeadArgs& a, int dtype) {
 // Cost of the three products of a piece of `words` words.
 template <typename T>
 double piece_cost(int64_t rows, int64_t words, int64_t dim) {
-    typedef typename LogitTile<T, true>::type ZLarge;
-    typedef typename LogitTile<T, false>::type ZSmall;
-    typedef typename TileFor<T, true, false, true>::type HLarge;
-    typedef typename TileFor<T, true, false, false>::type HSmall;
-    typedef typename TileFor<T, true, true, true>::type WLarge;
-    typedef typename TileFor<T, true, true, false>::type WSmall;
-    return cut_product<ZLarge, ZSmall>(words, rows, dim, false, kLogitEnds).cost +
-           cut_product<HLarge, HSmall>(dim, rows, words, true, kSumEnds).cost +
-           cut_product<WLarge, WSmall>(dim, words, rows, true, kSumEnds).cost;
+    return cut_logits<T>(words, rows, dim).cost + cut_gradient<T, false>(dim, rows, words).cost +
+           cut_gradient<T, true>(dim, words, rows).cost;
 }
 
 template <typename T>
@@ -1114,33 +1137,31 @@ hipError_t head_backward_t(const HeadArgs& a, int dtype, hipStream_t st) {
         head_small_backward_kernel<T><<<dim3((unsigned)(row_wgs + word_wgs)), 256, lds, st>>>(a, row_wgs);
         return hipGetLastError();
     }
-    typedef typename LogitTile<T, true>::type ZLarge;
-    typedef typename LogitTile<T, false>::type ZSmall;
-    typedef typename TileFor<T, true, false, true>::type HLarge;
-    typedef typename TileFor<T, true, false, false>::type HSmall;
-    typedef typename TileFor<T, true, true, true>::type WLarge;
-    typedef typename TileFor<T, true, true, false>::type WSmall;
     const int64_t cap = a.plan.packed;
     const bool in_place = reads_in_place(a.weight, a.wstride, a.D, dtype);
     const int step = in_place || a.plan.Vg < a.plan.Vw ? a.plan.Vg : a.plan.Vw;
     // grad_hidden's cut serves all pieces (their sums meet): the first is the largest
-    const Cut hc = cut_product<HLarge, HSmall>(a.D, a.N, a.V < step ? a.V : step, true, kSumEnds);
+    const Cut hc = cut_gradient<T, false>(a.D, a.N, a.V < step ? a.V : step);
     const hipError_t e = pack_rows<T>(a, cap, dtype == GR_BF16 ? kPackPlanes : kPackHalves + (a.gweight ? kPackPlanes : 0),
                                       a.ghidden && hc.splits == 1, st);
     if (e != hipSuccess) return e;
     for (int v = 0; v < a.V; v += step) {
         const int nv = a.V - v < step ? a.V - v : step;
         const Words W = words_operands<T>(a, v, nv, a.ghidden != nullptr, dtype, st);
-        if (cut_product<ZLarge, ZSmall>(nv, a.N, a.D, false, kLogitEnds).large) run_grad<ZLarge>(a, W.logits, cap, v, nv, st);
-        else run_grad<ZSmall>(a, W.logits, cap, v, nv, st);
+        const Shape z = cut_logits<T>(nv, a.N, a.D).shape;
+        if (z == kLarge) run_grad<typename LogitTile<T, kLarge>::type>(a, W.logits, cap, v, nv, st);
+        else if (z == kSmall) run_grad<typename LogitTile<T, kSmall>::type>(a, W.logits, cap, v, nv, st);
+        else run_grad<typename LogitTile<T, kDeep>::type>(a, W.logits, cap, v, nv, st);
         if (a.ghidden) {
-            if (hc.large) run_ghidden<T, HLarge>(a, W.planes, cap, v, nv, hc.splits, st);
-            else run_ghidden<T, HSmall>(a, W.planes, cap, v, nv, hc.splits, st);
+            if (hc.shape == kLarge) run_ghidden<T, typename TileFor<T, true, false, kLarge>::type>(a, W.planes, cap, v, nv, hc.splits, st);
+            else if (hc.shape == kSmall) run_ghidden<T, typename TileFor<T, true, false, kSmall>::type>(a, W.planes, cap, v, nv, hc.splits, st);
+            else run_ghidden<T, typename TileFor<T, true, false, kDeep>::type>(a, W.planes, cap, v, nv, hc.splits, st);
         }
         if (a.gweight) {
-            const Cut c = cut_product<WLarge, WSmall>(a.D, nv, a.N, true, kSumEnds);
-            if (c.large) run_gweight<T, WLarge>(a, cap, v, nv, c.splits, st);
-            else run_gweight<T, WSmall>(a, cap, v, nv, c.splits, st);
+            const Cut c = cut_gradient<T, true>(a.D, nv, a.N);
+            if (c.shape == kLarge) run_gweight<T, typename TileFor<T, true, true, kLarge>::type>(a, cap, v, nv, c.splits, st);
+            else if (c.shape == kSmall) run_gweight<T, typename TileFor<T, true, true, kSmall>::type>(a, cap, v, nv, c.splits, st);
+            else run_gweight<T, typename TileFor<T, true, true, kDeep>::type>(a, cap, v, nv, c.splits, st);
         }
     }
     if (a.ghidden && hc.splits > 1) head_ghidden_out_kernel<T><<<dim3((unsigned)a.N), 256, 0, st>>>(a, hc.splits);
