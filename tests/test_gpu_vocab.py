@@ -531,9 +531,10 @@ def test_scoring_head_is_the_training_heads_loss(gr, dtype, n):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n,vocab,dim", [(1_200_000, 70_000, 8), (3000, 5_000_000, 4), (20_000, 5000, 1024), (513, 2047, 8),
-                                         (600, 2048, 8), (900, 3, 6000)])
+                                         (600, 2048, 8), (900, 3, 6000), (1025, 70_000, 150), (2048, 1, 40),
+                                         (2048, 333, 25), (2049, 333, 25)])
 def test_embedding_of_many(gr, dtype, n, vocab, dim):
-    """Sorts of one, two and three passes, tiles of more than a few rows, whole
+    """Sorts by one workgroup and of one, two and three passes, tiles of more than a few rows, whole
     rows to a thread group, and lookups of four rows a group."""
     gen = _gen(n)
     t = _tokens(n, vocab, gen, 0.1)

@@ -18,6 +18,7 @@ struct EmbedLookupArgs {
 };
 
 constexpr int kEmbedFew = 512;    // at most so many tokens: no sort
+constexpr int kSortFew = 2048;    // at most so many: sorted by one workgroup
 constexpr int kSortBits = 11;     // of a sort pass at most
 constexpr int kSortChunk = 1024;  // positions of a sort workgroup
 constexpr int kSumTiles = 8192;   // tiles of the sums at most
