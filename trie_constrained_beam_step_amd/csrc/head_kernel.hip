@@ -829,13 +829,13 @@ __global__ __launch_bounds__(256) void head_zero_kernel(HeadArgs a) {
 
 // ------------------------------------------------------------ small problems
 
-// The whole backward in one launch, where several would cost more than the
-// work: a workgroup takes 16 rows of grad_hidden or 16 rows of grad_weight,
-// computes the slab of G it needs (so each logit is computed twice) into LDS in
-// fp32 and multiplies it.  fp32 matrix instructions throughout, bf16 elements
-// widened; no rounding of G.  48 rows, 48 words, 64 wide: 5.2 us, a chain of
-// loads.  A k of four is spread over a lane's four
-// consecutive elements: both operands agree on which.
+// The loss, or the whole backward, in one launch, where several would cost more
+// than the work.  Backward: a workgroup takes 16 rows of grad_hidden or 16 rows of
+// grad_weight, computes the slab of G it needs (so each logit is computed twice)
+// into LDS in fp32 and multiplies it.  fp32 matrix instructions throughout, bf16
+// elements widened; no rounding of G.  48 rows, 48 words, 64 wide: 5.2 us, a chain
+// of loads.  A k of four is spread over a lane's four consecutive elements: both
+// operands agree on which.
 constexpr int kSmallMost = 512;  // rows and words at most: their share of G is 33 KB of LDS
 
 __device__ __forceinline__ f32x4v load4(const float* p) { return *(const f32x4_anywhere*)p; }
@@ -845,6 +845,68 @@ __device__ __forceinline__ f32x4v load4(const uint16_t* p) {
     const u32x2 v = *(const Anywhere*)p;
     return f32x4v{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u), __uint_as_float(v[1] << 16),
                   __uint_as_float(v[1] & 0xFFFF0000u)};
+}
+
+// The logits (unscaled) of 16 words and 16 hidden states, each lane giving its
+// lane%16-th word v and state n: a lane gets words 4*(lane/16) .. +3 of its state,
+// zero where either is not in.  Loads are from clamped places and unconditional (a
+// branch around each would leave one in flight); what is not in is zeroed behind them.
+template <typename T>
+__device__ __forceinline__ f32x4v small_logits(const HeadArgs& a, int v, bool vin, int n, bool nin) {
+    const int lk = (threadIdx.x & 63) >> 4;
+    const T* wp = (const T*)a.weight + (int64_t)(vin ? v : 0) * a.wstride;
+    const T* hp = (const T*)a.hidden + (int64_t)(nin ? n : 0) * a.hstride;
+    f32x4v acc = {};
+    int d0 = 0;
+#pragma unroll 4
+    for (; d0 + 16 <= a.D; d0 += 16) {
+        const f32x4v x = load4(wp + d0 + lk * 4), y = load4(hp + d0 + lk * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin ? x[e] : 0.0f, nin ? y[e] : 0.0f, acc, 0, 0, 0);
+    }
+    for (; d0 < a.D; d0 += 16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int d = d0 + lk * 4 + e, at = min(d, a.D - 1);
+            const float x = load_elem(wp, at), y = load_elem(hp, at);
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin && d < a.D ? x : 0.0f, nin && d < a.D ? y : 0.0f, acc, 0, 0, 0);
+        }
+    }
+    return acc;
+}
+
+// The loss of a small problem: 16 rows to a workgroup, 16 threads to a row.  48
+// rows, 48 words, 64 wide: 4.1 us.  The backward below makes the same logits to
+// the bit, which leaves a probability near one as near to it: gradients of those
+// sizes are 3e-7 of their norm off where a loss by other sums left 1.1e-6.
+template <typename T>
+__global__ __launch_bounds__(256) void head_small_loss_kernel(HeadArgs a) {
+    extern __shared__ __align__(16) float zs[];  // [16][pitch]: rows x words
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, li = lane & 15, lk = lane >> 4;
+    const int r0 = blockIdx.x * 16, pitch = (a.V + 15) / 16 * 16 + 4;
+    const bool nin = has_target(a, r0 + li);
+    for (int v0 = wave * 16; v0 < a.V; v0 += 64) {
+        const f32x4v acc = small_logits<T>(a, v0 + li, v0 + li < a.V, r0 + li, nin);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) zs[li * pitch + v0 + lk * 4 + r] = acc[r] * a.scale;
+    }
+    __syncthreads();
+    const int row = threadIdx.x >> 4, c = threadIdx.x & 15, n = r0 + row;
+    const float* z = zs + row * pitch;
+    float m = kFarBelow, s = 0.0f;
+    for (int v = c; v < a.V; v += 16) m = fmaxf(m, z[v] * kLog2e);
+#pragma unroll
+    for (int o = 1; o < 16; o *= 2) m = fmaxf(m, __shfl_xor(m, o));
+    for (int v = c; v < a.V; v += 16) s += ex2(z[v] * kLog2e - m);
+#pragma unroll
+    for (int o = 1; o < 16; o *= 2) s += __shfl_xor(s, o);
+    if (c == 0 && n < a.N) {
+        const bool ok = has_target(a, n);
+        const float lse = ok ? lse_of(m, s) : 0.0f;
+        a.lse[n] = lse;
+        a.loss[n] = ok ? lse - z[a.targets[n]] : 0.0f;
+    }
 }
 
 template <typename T>
@@ -857,32 +919,12 @@ __global__ __launch_bounds__(256) void head_small_backward_kernel(HeadArgs a, in
     const int others = rows ? a.V : a.N;  // the length of the second product
     const int pitch = (others + 15) / 16 * 16 + 4;
 
-    // Loads are from clamped places and unconditional (a branch around each would
-    // leave one in flight); what does not exist is zeroed behind them.
     for (int o0 = wave * 16; o0 < others; o0 += 64) {
         const int v = (rows ? o0 : w0) + li, n = (rows ? r0 : o0) + li;
         const bool vin = v < a.V, nin = has_target(a, n);
-        const T* wp = (const T*)a.weight + (int64_t)(vin ? v : 0) * a.wstride;
-        const T* hp = (const T*)a.hidden + (int64_t)(nin ? n : 0) * a.hstride;
         const float g = nin ? a.scale * a.grad_loss[n] : 0.0f, lse = nin ? a.lse_in[n] : 0.0f;
         const int t = nin ? a.targets[n] - (v - li) : -1;
-        f32x4v acc = {};
-        int d0 = 0;
-#pragma unroll 4
-        for (; d0 + 16 <= a.D; d0 += 16) {
-            const f32x4v x = load4(wp + d0 + lk * 4), y = load4(hp + d0 + lk * 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin ? x[e] : 0.0f, nin ? y[e] : 0.0f, acc, 0, 0, 0);
-        }
-        for (; d0 < a.D; d0 += 16) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int d = d0 + lk * 4 + e, at = min(d, a.D - 1);
-                const float x = load_elem(wp, at), y = load_elem(hp, at);
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(vin && d < a.D ? x : 0.0f, nin && d < a.D ? y : 0.0f, acc, 0, 0, 0);
-            }
-        }
+        const f32x4v acc = small_logits<T>(a, v, vin, n, nin);
         // acc[r]: word 4*lk + r of the tile, row li
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -1034,9 +1076,22 @@ void run_parts(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, 
     head_parts_kernel<Tile><<<dim3((unsigned)(tiles_of(nv, Tile::BM) * tiles_of(a.N, Tile::BN))), Tile::NT, 0, st>>>(a, W, cap, v, nv);
 }
 
+// One launch: at most one workgroup to a CU, and no longer a walk of each wave
+// than the other way's launches cost.  A walk of 512: 4,096 fp32 rows of 512
+// against 64 words 12 us against 33, 512 bf16 rows of 64 against 512 words 14
+// against 16; of 2,000: 64 bf16 rows against 16 words 31 against 21, 64 fp32 rows
+// of 256 against 512 words 36 against 18.  16,384 bf16 rows of 512 against 64
+// words, four workgroups to a CU: 33 against 27.
+bool small_loss(const HeadArgs& a) { return a.N <= 4096 && a.V <= kSmallMost && (int64_t)tiles_of(a.V, 64) * a.D <= 512; }
+
 template <typename T>
 hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
     const int64_t cap = all.plan.part_rows;
+    if (small_loss(all)) {
+        const size_t lds = 16 * (size_t)(tiles_of(all.V, 16) * 16 + 4) * sizeof(float);
+        head_small_loss_kernel<T><<<dim3((unsigned)tiles_of(all.N, 16)), 256, lds, st>>>(all);
+        return hipGetLastError();
+    }
     for (int64_t r = 0; r < all.N; r += cap) {
         HeadArgs a = all;
         a.N = (int32_t)(all.N - r < cap ? all.N - r : cap);
