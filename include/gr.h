@@ -554,9 +554,10 @@ gr_status gr_head_loss(gr_head* head, const void* d_hidden, int64_t hidden_row_s
  *   grad_weight[v] = sum_n G[n][v] * hidden[n]     (+ what it holds, if accumulate != 0)
  * d_lse is gr_head_loss's of the same inputs.  The logits are computed again,
  * a piece of the vocabulary at a time.  For bf16, a piece's G may be rounded
- * to bf16 before both products (half a step of each of its elements).  d_grad_hidden or d_grad_weight may be NULL
- * (not both): that gradient is then not computed.  n = 0 writes zeros to
- * grad_weight unless accumulate.  GR_ERR_UNSUPPORTED for a score_only head.
+ * to bf16 before both products (half a step of each of its elements).
+ * d_grad_hidden or d_grad_weight may be NULL (not both): that gradient is then
+ * not computed.  n = 0 writes zeros to grad_weight unless accumulate.
+ * GR_ERR_UNSUPPORTED for a score_only head.
  */
 gr_status gr_head_backward(gr_head* head, const void* d_hidden, int64_t hidden_row_stride, const void* d_weight,
                            int64_t weight_row_stride, const int32_t* d_targets, int32_t n, const float* d_lse,

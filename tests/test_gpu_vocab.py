@@ -128,7 +128,7 @@ def test_embedding_gradient_without_rows(gr, dtype, tokens):
 
 HEADS = [(1, 48, 64), (48, 48, 64), (1, 1, 1), (3, 5, 7), (17, 1280, 96), (16, 513, 128), (33, 300, 1000),
          (65, 1000, 67), (130, 257, 256), (300, 770, 200), (700, 130, 64), (257, 2100, 130),
-         (4096, 64, 512), (4097, 64, 512), (9, 512, 64), (200, 449, 63), (35, 15, 500)]
+         (4096, 64, 512), (4097, 64, 512), (9, 512, 64), (200, 449, 63), (35, 15, 256), (64, 256, 64), (65, 257, 64)]
 
 
 def _head_inputs(n, vocab, dim, dtype, seed, absent=0.2):

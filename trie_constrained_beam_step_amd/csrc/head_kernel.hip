@@ -1081,8 +1081,12 @@ void run_parts(const HeadArgs& a, const Operand& W, int64_t cap, int v, int nv, 
 // against 64 words 12 us against 33, 512 bf16 rows of 64 against 512 words 14
 // against 16; of 2,000: 64 bf16 rows against 16 words 31 against 21, 64 fp32 rows
 // of 256 against 512 words 36 against 18.  16,384 bf16 rows of 512 against 64
-// words, four workgroups to a CU: 33 against 27.
-bool small_loss(const HeadArgs& a) { return a.N <= 4096 && a.V <= kSmallMost && (int64_t)tiles_of(a.V, 64) * a.D <= 512; }
+// words, four workgroups to a CU: 33 against 27.  Up to kFewRows rows the other way
+// is two launches, and the walk 256: 8 bf16 rows of 64 against 512 words (a walk of
+// 512), 3.7 and 4.2 us of kernels by it against 11.6.
+bool small_loss(const HeadArgs& a) {
+    return a.N <= 4096 && a.V <= kSmallMost && (int64_t)tiles_of(a.V, 64) * a.D <= (a.N <= kFewRows ? 256 : 512);
+}
 
 template <typename T>
 hipError_t head_loss_t(const HeadArgs& all, int dtype, hipStream_t st) {
